@@ -232,6 +232,64 @@ int mlra_project_append(mlra_handle h, const void* x, int d_model, const void* w
                         const int32_t* positions, void* pool, int num_pages, const int32_t* page_table,
                         int pt_stride, int batch, void* workspace, size_t ws_bytes, void* stream);
 
+/* Bytes of device workspace mlra_prefill needs (host output): about 80 KB a query token with 128
+ * heads of 128 (packed query and latent result), plus a fixed part of some 40 MB; with an E4M3
+ * cache also the bf16 form of batch * pt_stride pages. */
+int mlra_prefill_workspace_size(mlra_handle h, int total_q, int batch, int pt_stride, size_t* bytes);
+
+/* Causal attention of the query tokens of packed sequences (whole prompts, or the next tokens of
+ * longer contexts) over the sequences' cached rows, which must be in the cache already
+ * (mlra_append_cache), the query tokens' own among them. Same formulas as the decode step:
+ *   query token i of sequence b, n_b = cu_seqlens[b+1] - cu_seqlens[b] of them, has position
+ *   pos = seq_lens[b] - n_b + i and attends to the cached rows 0 .. pos. A token whose position
+ *   is negative attends to nothing: o = 0, lse = -inf.
+ *   q          device [total_q][h][d_h + d_rope], as in mlra_decode, sequence after sequence.
+ *              16-byte aligned. total_q <= 2^21. An fp32 query is rounded to bf16.
+ *   cu_seqlens device int32 [batch + 1], ascending from 0 to at most total_q; sequence b's tokens
+ *              are rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (none: n_b = 0). Rows from
+ *              cu_seqlens[batch] on belong to no sequence; their out and lse stay as they were.
+ *              Offsets that do not ascend leave all of out and lse as they were and report
+ *              MLRA_ERR_SEQ_LEN.
+ *   pool, num_pages, page_table, pt_stride: as in mlra_decode. Sequences may share pages.
+ *   seq_lens   device int32 [batch], 0 <= len <= pt_stride * page_size; outside it is clamped and
+ *              MLRA_ERR_SEQ_LEN reported.
+ *   out        device [total_q][h][d_h], dtype out_dtype, 16-byte aligned.
+ *   lse        device fp32 [total_q][h] ([total_q][k*h], block-major, with blocks_summed), natural
+ *              log, or NULL.
+ *   workspace  device, >= mlra_prefill_workspace_size bytes, 256-byte aligned; its first 4 bytes
+ *              become this call's status word.
+ * A row of the cache that holds NaN or infinities reaches only the tokens that attend to it.
+ * Launches five kernels on `stream` (six with an E4M3 cache), chained by programmatic dependent
+ * launch: query absorption, the split plan, the attention, the merge of split results and the
+ * up-projection. The result does not depend on timing. batch <= 4096. */
+int mlra_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t* cu_seqlens, int total_q,
+                 const void* pool, int num_pages, const int32_t* page_table, int pt_stride, const int32_t* seq_lens,
+                 int batch, void* out, mlra_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes,
+                 void* stream);
+
+/* Bytes of device workspace mlra_decode_prefix needs (host output). */
+int mlra_decode_prefix_workspace_size(mlra_handle h, int batch, int groups, size_t* bytes);
+
+/* One decode step of a batch whose sequences share long prefixes in groups (samples of one
+ * prompt, requests behind one system prompt). Group g is the sequences group_offsets[g] ..
+ * group_offsets[g+1] - 1; sequence b of group g attends to the prefix_lens[g] cached rows of
+ * prefix_table's row g, then to its own seq_lens[b] cached rows of page_table's row b: the result
+ * is mlra_decode's on the two laid end to end (RoPE is in the cached rows already). The prefix is
+ * read and attended to once for all its members.
+ *   prefix_table  device int32 [groups][prefix_stride], prefix_lens device int32 [groups]: laid out
+ *                 as page_table and seq_lens are. A prefix may end within a page.
+ *   group_offsets device int32 [groups + 1], ascending from 0 to at most batch. Sequences behind
+ *                 the last group have no prefix. Offsets that do not ascend report
+ *                 MLRA_ERR_SEQ_LEN and every sequence is then decoded without a prefix.
+ *   seq_lens      own rows only, may be 0; a sequence with neither gives o = 0, lse = -inf.
+ * Other arguments as in mlra_decode; workspace >= mlra_decode_prefix_workspace_size bytes. bf16
+ * caches only (MLRA_ERR_UNSUPPORTED with cache_fp8); batch <= 4096, groups <= 4096. */
+int mlra_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const void* pool, int num_pages,
+                       const int32_t* prefix_table, int prefix_stride, const int32_t* prefix_lens,
+                       const int32_t* group_offsets, int groups, const int32_t* page_table, int pt_stride,
+                       const int32_t* seq_lens, int batch, void* out, mlra_dtype out_dtype, float* lse,
+                       void* workspace, size_t ws_bytes, void* stream);
+
 /* Runs the device split planner on seq_lens and writes the segments it would process:
  * segments device int32 [max_segments][5] rows (b, group, tile_begin, tile_end, slot),
  * count device int32. A group is a set of CTAs that shares one run of 128-token tiles;

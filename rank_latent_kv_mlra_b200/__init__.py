@@ -37,6 +37,7 @@ EXPORTED = [
     "mlra_create", "mlra_destroy", "mlra_workspace_size", "mlra_decode", "mlra_decode_latent",
     "mlra_append_cache", "mlra_plan", "mlra_get_info", "mlra_get_status", "mlra_status_string",
     "mlra_decode_profiled", "mlra_decode_noalloc", "mlra_project_workspace_size", "mlra_project_append",
+    "mlra_prefill_workspace_size", "mlra_prefill", "mlra_decode_prefix_workspace_size", "mlra_decode_prefix",
 ]
 
 
@@ -84,6 +85,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mlra_append_cache.argtypes = [P, P, I, P, I, I, P, P, P, P, I, I, P, P]
     lib.mlra_project_workspace_size.argtypes = [P, I, I, ctypes.POINTER(S)]
     lib.mlra_project_append.argtypes = [P, P, I, P, ctypes.c_float, P, P, I, P, I, I, P, S, P]
+    lib.mlra_prefill_workspace_size.argtypes = [P, I, I, I, ctypes.POINTER(S)]
+    lib.mlra_prefill.argtypes = [P, P, I, P, I, P, I, P, I, P, I, P, I, P, P, S, P]
+    lib.mlra_decode_prefix_workspace_size.argtypes = [P, I, I, ctypes.POINTER(S)]
+    lib.mlra_decode_prefix.argtypes = [P, P, I, P, I, P, I, P, P, I, P, I, P, I, P, I, P, P, S, P]
     lib.mlra_plan.argtypes = [P, P, I, I, P, I, P, P]
     lib.mlra_get_info.argtypes = [P, ctypes.POINTER(mlra_info)]
     lib.mlra_get_status.argtypes = [P, ctypes.POINTER(I)]
@@ -324,6 +329,118 @@ def mlra_project_append(handle: Handle, x, w_down, positions, pool, page_table, 
         handle.ptr, _ptr(x), d_model, _ptr(w_down), float(rope_base), _ptr(positions), _ptr(pool),
         pool.shape[0], _ptr(page_table), page_table.shape[1], B, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)), "mlra_project_append")
+    return workspace
+
+
+def _on_one_device(**tensors):
+    """The device all of these tensors (None allowed) are on."""
+    devs = {t.device for t in tensors.values() if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"{', '.join(tensors)} must be on one device")
+    return devs.pop()
+
+
+def _workspace(workspace, size: int, device, stream):
+    """The caller's workspace, or one of `size` bytes that outlives the work on `stream`."""
+    if workspace is not None:
+        _require(workspace, "workspace")
+        return workspace
+    workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    if stream is not None:
+        workspace.record_stream(stream)
+    return workspace
+
+
+def mlra_prefill_workspace_size(handle: Handle, total_q: int, batch: int, pt_stride: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().mlra_prefill_workspace_size(handle.ptr, total_q, batch, pt_stride, ctypes.byref(n)),
+           "mlra_prefill_workspace_size")
+    return n.value
+
+
+def _attention_args(handle, q, q_rows, pool, out, lse):
+    cfg = handle.cfg
+    _require(q, "q")
+    _require(pool, "pool", _pool_dtype(handle))
+    _require(out, "out")
+    if tuple(q.shape) != (q_rows, cfg.h, cfg.d_h + cfg.d_rope):
+        raise ValueError("q must be [tokens][h][d_h + d_rope]")
+    if tuple(out.shape) != (q_rows, cfg.h, cfg.d_h):
+        raise ValueError("out must be [tokens][h][d_h]")
+    if pool.dim() != 3 or pool.shape[1] != cfg.page_size or pool.shape[2] != cfg.d_c + cfg.d_rope:
+        raise ValueError("pool must be [num_pages][page_size][d_c + d_rope]")
+    if lse is not None:
+        _require(lse, "lse", torch.float32)
+        if lse.numel() != q_rows * cfg.h * (cfg.k if cfg.blocks_summed else 1):
+            raise ValueError("lse must be [tokens][h], or [tokens][k*h] with summed blocks")
+
+
+def _tables(page_table, seq_lens, names):
+    _require(page_table, names[0], torch.int32)
+    _require(seq_lens, names[1], torch.int32)
+    if page_table.dim() != 2 or seq_lens.shape != (page_table.shape[0],):
+        raise ValueError(f"{names[0]} must be [sequences][stride], {names[1]} [sequences]")
+
+
+def mlra_prefill(handle: Handle, q, cu_seqlens, pool, page_table, seq_lens, out, lse=None, workspace=None,
+                 stream=None):
+    """Causal attention of packed prompt tokens over their sequences' cached rows. Rows
+    cu_seqlens[b] .. cu_seqlens[b+1] - 1 of `q` [total][h][d_h + d_rope] are the last tokens of
+    sequence b, whose seq_lens[b] cached rows include their own; `out` [total][h][d_h] (fp32 or
+    bf16), `lse` fp32 [total][h] ([total][k*h] with summed blocks) or None. Rows of q behind
+    cu_seqlens[batch] are not read and their out and lse are left as they were. Returns the
+    workspace, whose first int32 is the call's status word."""
+    total = q.shape[0]
+    _attention_args(handle, q, total, pool, out, lse)
+    _tables(page_table, seq_lens, ("page_table", "seq_lens"))
+    _require(cu_seqlens, "cu_seqlens", torch.int32)
+    B = page_table.shape[0]
+    if cu_seqlens.shape != (B + 1,):
+        raise ValueError("cu_seqlens must be [batch + 1]")
+    dev = _on_one_device(q=q, cu_seqlens=cu_seqlens, pool=pool, page_table=page_table, seq_lens=seq_lens, out=out,
+                         lse=lse, workspace=workspace)
+    with torch.cuda.device(dev):
+        workspace = _workspace(workspace, 0 if workspace is not None else
+                               mlra_prefill_workspace_size(handle, total, B, page_table.shape[1]), dev, stream)
+        _check(load_library().mlra_prefill(
+            handle.ptr, _ptr(q), _dtype(q), _ptr(cu_seqlens), total, _ptr(pool), pool.shape[0], _ptr(page_table),
+            page_table.shape[1], _ptr(seq_lens), B, _ptr(out), _dtype(out), _ptr(lse), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream)), "mlra_prefill")
+    return workspace
+
+
+def mlra_decode_prefix_workspace_size(handle: Handle, batch: int, groups: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().mlra_decode_prefix_workspace_size(handle.ptr, batch, groups, ctypes.byref(n)),
+           "mlra_decode_prefix_workspace_size")
+    return n.value
+
+
+def mlra_decode_prefix(handle: Handle, q, pool, prefix_table, prefix_lens, group_offsets, page_table, seq_lens, out,
+                       lse=None, workspace=None, stream=None):
+    """One decode step of a batch whose sequences share prefixes: sequences group_offsets[g] ..
+    group_offsets[g+1] - 1 attend to the prefix_lens[g] cached rows that prefix_table's row g
+    names, then to their own seq_lens[b] rows in page_table's row b. A prefix is attended to
+    once for all its members. `out` and `lse` as in mlra_decode. Returns the workspace."""
+    B = q.shape[0]
+    _attention_args(handle, q, B, pool, out, lse)
+    _tables(page_table, seq_lens, ("page_table", "seq_lens"))
+    _tables(prefix_table, prefix_lens, ("prefix_table", "prefix_lens"))
+    _require(group_offsets, "group_offsets", torch.int32)
+    G = prefix_table.shape[0]
+    if page_table.shape[0] != B or group_offsets.shape != (G + 1,):
+        raise ValueError("page_table must be [batch][stride], group_offsets [groups + 1]")
+    dev = _on_one_device(q=q, pool=pool, prefix_table=prefix_table, prefix_lens=prefix_lens,
+                         group_offsets=group_offsets, page_table=page_table, seq_lens=seq_lens, out=out, lse=lse,
+                         workspace=workspace)
+    with torch.cuda.device(dev):
+        workspace = _workspace(workspace, 0 if workspace is not None else
+                               mlra_decode_prefix_workspace_size(handle, B, G), dev, stream)
+        _check(load_library().mlra_decode_prefix(
+            handle.ptr, _ptr(q), _dtype(q), _ptr(pool), pool.shape[0], _ptr(prefix_table), prefix_table.shape[1],
+            _ptr(prefix_lens), _ptr(group_offsets), G, _ptr(page_table), page_table.shape[1], _ptr(seq_lens), B,
+            _ptr(out), _dtype(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _stream(stream)), "mlra_decode_prefix")
     return workspace
 
 

@@ -20,6 +20,7 @@
 #include "producer.cuh"
 #include "decode.cuh"
 #include "proj.cuh"
+#include "rows.cuh"
 
 using namespace mlra;
 
@@ -375,7 +376,7 @@ int run_decode(mlra_handle h, const void* q, mlra_dtype q_dtype, const void* poo
   pp.q = q;
   pp.q_f32 = q_dtype == MLRA_F32;
   pp.q_pack = w.q_pack;
-  pp.qscale = h->scale * kLog2e;
+  pp.qscale = pp.qscale_rope = h->scale * kLog2e;
   pp.d_r = h->d_r;
   pp.np = h->np;
   pp.nsub = h->nsub;
@@ -574,6 +575,8 @@ cudaError_t launch_down_proj(const CUtensorMap& mw, const CUtensorMap& mx, const
 }
 }  // namespace
 
+#include "rows_api.cuh"
+
 extern "C" {
 
 int mlra_create(const mlra_config* cfg, const void* w_uk, const void* w_uv, mlra_handle* out) {
@@ -682,6 +685,8 @@ int mlra_create(const mlra_config* cfg, const void* w_uk, const void* w_uv, mlra
       break;
   }
   if (e == cudaSuccess) e = prep_producer();
+  if (e == cudaSuccess) e = prep_rows(h->var);
+  if (e == cudaSuccess) e = prep_prefix(h->var, summed);
   if (e != cudaSuccess) {
     delete h;
     return MLRA_ERR_CUDA;
@@ -741,6 +746,36 @@ int mlra_decode_latent(mlra_handle h, const void* q, mlra_dtype q_dtype, const v
   if (!latent_out) return MLRA_ERR_INVALID_ARG;
   return run_decode(h, q, q_dtype, pool, num_pages, page_table, pt_stride, seq_lens, batch, nullptr,
                     MLRA_F32, lse, latent_out, workspace, ws_bytes, stream, 0, kWaitLimitNs);
+}
+
+int mlra_prefill_workspace_size(mlra_handle h, int total_q, int batch, int pt_stride, size_t* bytes) {
+  if (!h || !bytes || !rows_sizes_ok(total_q, batch, pt_stride)) return MLRA_ERR_INVALID_ARG;
+  *bytes = carve_prefill(h, total_q, batch, pt_stride, nullptr).bytes;
+  return MLRA_OK;
+}
+
+int mlra_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t* cu_seqlens, int total_q,
+                 const void* pool, int num_pages, const int32_t* page_table, int pt_stride, const int32_t* seq_lens,
+                 int batch, void* out, mlra_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes,
+                 void* stream) {
+  return run_prefill(h, q, q_dtype, cu_seqlens, total_q, pool, num_pages, page_table, pt_stride, seq_lens, batch, out,
+                     out_dtype, lse, workspace, ws_bytes, stream);
+}
+
+int mlra_decode_prefix_workspace_size(mlra_handle h, int batch, int groups, size_t* bytes) {
+  if (!h || !bytes || batch <= 0 || batch > 4096 || groups <= 0 || groups > kMaxSeqs) return MLRA_ERR_INVALID_ARG;
+  *bytes = carve_prefix(h, batch, groups, nullptr).bytes;
+  return MLRA_OK;
+}
+
+int mlra_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const void* pool, int num_pages,
+                       const int32_t* prefix_table, int prefix_stride, const int32_t* prefix_lens,
+                       const int32_t* group_offsets, int groups, const int32_t* page_table, int pt_stride,
+                       const int32_t* seq_lens, int batch, void* out, mlra_dtype out_dtype, float* lse,
+                       void* workspace, size_t ws_bytes, void* stream) {
+  return run_decode_prefix(h, q, q_dtype, pool, num_pages, prefix_table, prefix_stride, prefix_lens, group_offsets,
+                           groups, page_table, pt_stride, seq_lens, batch, out, out_dtype, lse, workspace, ws_bytes,
+                           stream);
 }
 
 int mlra_append_cache(mlra_handle h, void* pool, int num_pages, const int32_t* page_table, int pt_stride,

@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "decode.cuh"
+#include "rowplan.cuh"
 
 namespace mlra {
 
@@ -27,12 +28,24 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kProjThreads = 512;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Where the attention over shared prefixes left its results: whole units in dense rows, cut ones
+// in the slots of the CTAs that worked on them.
+struct PrefixParts {
+  RowPlan plan;
+  int ctas, units, halves, chunks, heads_tile, tok_tile, key_tile, rows, dv;
+  const float* o_dense;   // [batch][h][DB]
+  const float* lse_dense; // [batch][h] log2
+  const float* part_o;    // [2 * ctas][rows][dv]
+  const float* part_lse;  // [2 * ctas][rows] log2
+};
+
 struct ProjParams {
   // absorb
   const void* q;      // [B][h][d_h + d_r]
   int q_f32;          // 1: fp32 q, 0: bf16 q
   __nv_bfloat16* q_pack;  // [B][nsub][NP][DB + DR]
-  float qscale;       // softmax scale * log2(e)
+  float qscale;       // softmax scale * log2(e), of q^C
+  float qscale_rope;  // of q^R (bf16 packed query)
   int d_r;
   int np;             // heads per decode CTA (rows per q_pack block)
   int nsub;           // decode CTAs per group
@@ -60,6 +73,8 @@ struct ProjParams {
   float rope_scale;    // value of a RoPE byte = rope_scale * e4m3(byte)
   float* qfac;         // [B][nsub][np] factor of each head's query terms
   int q_rows_per_sub;  // query rows per (sequence, decode CTA): np, or 2 * np for two terms
+  // parts of a prefix that sequences share (combine with PREFIX; see rows.cuh)
+  PrefixParts prefix;
   int* status;        // cleared by absorb CTA (0, 0); written by the combine kernel
   EarlyTags tags;     // absorb errors (the decode kernel folds them into status)
   unsigned long long wait_limit_ns;
@@ -243,10 +258,10 @@ __global__ void __launch_bounds__(kProjThreads, 1)
           for (int e = 0; e < 8; ++e) stf[bl * qw + DB + (d8 - DH) + e] = v[i][e] * p.qscale * p.rope_scale;
         } else if (n0 + bl < p.batch) {
           uint4 w;
-          w.x = pack_bf16x2(v[i][0] * p.qscale, v[i][1] * p.qscale);
-          w.y = pack_bf16x2(v[i][2] * p.qscale, v[i][3] * p.qscale);
-          w.z = pack_bf16x2(v[i][4] * p.qscale, v[i][5] * p.qscale);
-          w.w = pack_bf16x2(v[i][6] * p.qscale, v[i][7] * p.qscale);
+          w.x = pack_bf16x2(v[i][0] * p.qscale_rope, v[i][1] * p.qscale_rope);
+          w.y = pack_bf16x2(v[i][2] * p.qscale_rope, v[i][3] * p.qscale_rope);
+          w.z = pack_bf16x2(v[i][4] * p.qscale_rope, v[i][5] * p.qscale_rope);
+          w.w = pack_bf16x2(v[i][6] * p.qscale_rope, v[i][7] * p.qscale_rope);
           *reinterpret_cast<uint4*>(p.q_pack + (((size_t)(n0 + bl) * p.nsub + sub) * p.np + prow) * qw + DB +
                                     (d8 - DH)) = w;
         }
@@ -303,8 +318,8 @@ __global__ void __launch_bounds__(kProjThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 v = __bfloat1622float2(h2[e]);
-          f[2 * e] = v.x * p.qscale;
-          f[2 * e + 1] = v.y * p.qscale;
+          f[2 * e] = v.x * (F8 ? p.qscale : p.qscale_rope);
+          f[2 * e + 1] = v.y * (F8 ? p.qscale : p.qscale_rope);
         }
         if constexpr (F8) {
 #pragma unroll
@@ -428,7 +443,8 @@ __global__ void __launch_bounds__(kProjThreads, 1)
 // virtual heads j*out_heads + head (latent block j), lays them side by side along K
 // (DB = SUMK * block width) and multiplies by the SUMK stacked W^UV matrices in one GEMM, so
 // the sum over blocks happens in the tensor core's accumulator; out_scale applies alpha_attn.
-template <class Sh, bool LATENT_ONLY, int SUMK = 1>
+// PREFIX: after a sequence's own partials come the parts of the prefix it shares with others.
+template <class Sh, bool LATENT_ONLY, int SUMK = 1, bool PREFIX = false>
 __global__ void __launch_bounds__(kProjThreads, 1)
     mlra_uproj_kernel(const __grid_constant__ CUtensorMap map_wuv, const ProjParams p) {
   constexpr int DB = Sh::DB, DH = Sh::DH, NT = Sh::NT;
@@ -547,6 +563,35 @@ __global__ void __launch_bounds__(kProjThreads, 1)
         }
       }
     }
+    // the prefix's parts: CTAs px0 .. px0 + npx - 1 (npx = 0: none, 1 with px0 < 0: a whole unit)
+    int px0[RB], npx[RB], prow[RB];
+    if constexpr (PREFIX) {
+      const PrefixParts& pp = p.prefix;
+      const long long total = __ldg(pp.plan.start + __ldg(pp.plan.hdr));
+      const long long pquota = total > 0 ? (total + pp.ctas - 1) / pp.ctas : 1;
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        const int bl = r0 + rb, b = n0 + bl;
+        px0[rb] = -1;
+        npx[rb] = prow[rb] = 0;
+        const int ti = bl < NT && b < p.batch ? __ldg(pp.plan.tok_tile + b) : -1;
+        if (ti < 0) continue;
+        const TokenTile t = pp.plan.tile[ti];
+        const int kv = key_tiles(t, 0, pp.key_tile);
+        if (kv == 0) continue;
+        const int blk = vhead / p.heads_block, hb = vhead % p.heads_block;
+        const int usub = (blk * pp.chunks + hb / pp.heads_tile) * pp.halves + f0 / pp.dv;
+        const long long first = __ldg(pp.plan.start + ti) + (long long)usub * unit_cost(kv) + kUnitCost;
+        const int x0 = (int)(first / pquota), x1 = (int)((first + kv - 1) / pquota);
+        const int tok = b - t.tok0;
+        prow[rb] = (tok / pp.tok_tile) * 128 + (tok % pp.tok_tile) * pp.heads_tile + hb % pp.heads_tile;
+        npx[rb] = x1 - x0 + 1;
+        if (x1 > x0) px0[rb] = x0;
+      }
+    } else {
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) px0[rb] = npx[rb] = prow[rb] = 0;
+    }
     float acc[RB][PER];
     float mx[RB], sum[RB];
 #pragma unroll
@@ -558,7 +603,7 @@ __global__ void __launch_bounds__(kProjThreads, 1)
     }
     int maxseg = 0;
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) maxseg = max(maxseg, nsg[rb]);
+    for (int rb = 0; rb < RB; ++rb) maxseg = max(maxseg, nsg[rb] + npx[rb]);
     if (threadIdx.x == 0) MLRA_TRACE_POINT(2, 7);
     for (int s0 = 0; s0 < maxseg; s0 += SB) {
       float lv[RB][SB];
@@ -582,6 +627,15 @@ __global__ void __launch_bounds__(kProjThreads, 1)
 #pragma unroll
               for (int e = 0; e < PER; ++e) v[rb][si][e] = __ldg(src + e);
             }
+          } else if (PREFIX && s0 + si < nsg[rb] + npx[rb]) {
+            const int x = s0 + si - nsg[rb];
+            const PrefixParts& pp = p.prefix;
+            const size_t whole = (size_t)b * p.h + vhead;
+            const size_t cut = (size_t)(2 * (px0[rb] + x) + (x == 0 ? 1 : 0)) * pp.rows + prow[rb];
+            lv[rb][si] = __ldg(px0[rb] < 0 ? pp.lse_dense + whole : pp.part_lse + cut);
+            const float* src = px0[rb] < 0 ? pp.o_dense + whole * DBB + f0 : pp.part_o + cut * pp.dv + f0 % pp.dv;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) v[rb][si][e] = __ldg(src + e);
           } else {
             lv[rb][si] = -INFINITY;
 #pragma unroll
@@ -621,7 +675,8 @@ __global__ void __launch_bounds__(kProjThreads, 1)
 #pragma unroll
       for (int e = 0; e < PER; ++e) acc[rb][e] *= inv;
       if (b < p.batch && f0 == 0 && p.lse_out)  // one lane per (virtual) head
-        p.lse_out[(size_t)b * p.h + vhead] = nsg[rb] > 0 ? (mx[rb] + __log2f(sum[rb])) * kLn2 : -INFINITY;
+        p.lse_out[(size_t)b * p.h + vhead] =
+            nsg[rb] + npx[rb] > 0 ? (mx[rb] + __log2f(sum[rb])) * kLn2 : -INFINITY;
       if constexpr (LATENT_ONLY) {
         if (b < p.batch) {
           float* dst = p.latent_out + ((size_t)b * p.h + head) * DB + lane * PER;

@@ -1,0 +1,218 @@
+// rowplan.cuh - the split of attention over many query rows: token tiles, units, and the stretch of
+// units that each CTA of the attention kernel takes (see rows.cuh).
+#pragma once
+
+#include "common.cuh"
+
+namespace mlra {
+
+// cost of a unit beyond its key tiles, in key tiles: query load, pipeline fill and epilogue
+constexpr int kUnitCost = 1;
+
+// ---------------------------------------------------------------------------------------
+// The plan
+// ---------------------------------------------------------------------------------------
+// A token tile: `ntok` query tokens from `tok0` (row index into the packed queries) of sequence b.
+// Token i of the tile sees keys [0, lim0 + i) when causal, [0, lim0) otherwise (lim0 may be <= 0).
+struct TokenTile {
+  int b, tok0, ntok, lim0;
+};
+struct RowPlan {
+  int* hdr;            // [0] token tiles, [1] tokens in use (cu[batch]), [2] bad lengths found
+  long long* start;    // [max tiles + 1] position of each tile's first unit; the last is the total
+  TokenTile* tile;     // [max tiles]
+  int* tok_tile;       // [tokens] tile of each token, or null
+};
+struct RowPlanParams {
+  const int* cu;       // [batch + 1] first query token of each sequence
+  const int* lens;     // [batch] cached tokens of each sequence
+  int batch, total_q, cap_len;
+  int tile_tokens, key_tile, units;  // tokens a token tile, keys a key tile, units a token tile
+  int causal;
+  RowPlan plan;
+  int* status;
+};
+
+__device__ __forceinline__ int tile_limit(const TokenTile& t, int causal) {
+  const int l = causal ? t.lim0 + t.ntok - 1 : t.lim0;
+  return l > 0 ? l : 0;
+}
+__device__ __forceinline__ int key_tiles(const TokenTile& t, int causal, int key_tile) {
+  return (tile_limit(t, causal) + key_tile - 1) / key_tile;
+}
+__device__ __forceinline__ int unit_cost(int kv) { return kv > 0 ? kv + kUnitCost : 0; }
+
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxSeqs = 4096;
+
+template <class T>
+__device__ __forceinline__ T block_exclusive_scan(T v, T* scratch, T* total) {
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane_id() >= o) x += y;
+  }
+  __syncthreads();
+  if (lane_id() == 31) scratch[warp_id()] = x;
+  __syncthreads();
+  T before = 0, all = 0;
+  const int nw = blockDim.x >> 5;
+  for (int w = 0; w < nw; ++w) {
+    if (w < warp_id()) before += scratch[w];
+    all += scratch[w];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+// One CTA. Bounded by latency: a block scan per 1024 token tiles.
+__global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const RowPlanParams p) {
+  __shared__ int base[kMaxSeqs + 1];  // first token tile of each sequence
+  __shared__ long long scratch[32];
+  __shared__ int scratch_i[32];
+  __shared__ int flags[2];
+  if (threadIdx.x < 2) flags[threadIdx.x] = 0;
+  __syncthreads();
+  grid_launch_dependents();
+  // This kernel's inputs were there before the call and its outputs are read by later kernels of
+  // the call only; the kernel in front of it (absorb) waited for the work before the call.
+  int bad = 0;  // 1: a length outside its table row; 2: cu not ascending within [0, total_q]
+  int running = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    int tiles = 0;
+    if (b < p.batch) {
+      const int lo = p.cu[b], hi = p.cu[b + 1], n = p.lens[b];
+      if (lo < 0 || hi < lo || hi > p.total_q || (b == 0 && lo != 0)) bad |= 2;
+      else tiles = (hi - lo + p.tile_tokens - 1) / p.tile_tokens;
+      if (n < 0 || n > p.cap_len) bad |= 1;
+    }
+    int all;
+    const int first = running + block_exclusive_scan<int>(tiles, scratch_i, &all);
+    if (b < p.batch) base[b] = first;
+    running += all;
+  }
+  if (bad) atomicOr(&flags[0], bad);
+  if (p.plan.tok_tile != nullptr)  // tokens of no sequence
+    for (int i = threadIdx.x; i < p.total_q; i += kPlanThreads) p.plan.tok_tile[i] = -1;
+  __syncthreads();
+  // packed offsets that do not ascend leave no work at all
+  const int tiles = (flags[0] & 2) ? 0 : running;
+  if (threadIdx.x == 0) base[p.batch] = running;
+  __syncthreads();
+  long long pos = 0;
+  for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    long long cost = 0;
+    TokenTile t = {0, 0, 0, 0};
+    if (i < tiles) {
+      int lo = 0, hi = p.batch;  // last b with base[b] <= i
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (base[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      const int c0 = p.cu[lo], n_q = p.cu[lo + 1] - c0;
+      int len = p.lens[lo];
+      len = len < 0 ? 0 : len > p.cap_len ? p.cap_len : len;
+      const int first = (i - base[lo]) * p.tile_tokens;
+      t.b = lo;
+      t.tok0 = c0 + first;
+      t.ntok = min(p.tile_tokens, n_q - first);
+      t.lim0 = p.causal ? len - n_q + first + 1 : len;
+      cost = (long long)unit_cost(key_tiles(t, p.causal, p.key_tile)) * p.units;
+    }
+    long long all;
+    const long long at = pos + block_exclusive_scan<long long>(cost, scratch, &all);
+    if (i < tiles) {
+      p.plan.start[i] = at;
+      p.plan.tile[i] = t;
+      if (p.plan.tok_tile != nullptr)
+        for (int j = 0; j < t.ntok; ++j) p.plan.tok_tile[t.tok0 + j] = i;
+    }
+    pos += all;
+  }
+  if (threadIdx.x == 0) {
+    p.plan.start[tiles] = pos;
+    p.plan.hdr[0] = tiles;
+    p.plan.hdr[1] = (flags[0] & 2) ? 0 : p.cu[p.batch];
+    p.plan.hdr[2] = flags[0];
+  }
+  grid_dependency_wait();  // the absorb kernel clears the status word
+  if (threadIdx.x == 0 && flags[0]) set_status(p.status, kErrSeqLen);
+}
+
+// A CTA's stretch of the line of units.
+struct Stretch {
+  long long lo, hi, quota;
+};
+__device__ __forceinline__ Stretch stretch_of(long long total, int cta, int ctas) {
+  Stretch s;
+  s.quota = total > 0 ? (total + ctas - 1) / ctas : 1;
+  s.lo = min((long long)cta * s.quota, total);
+  s.hi = min(s.lo + s.quota, total);
+  return s;
+}
+
+// One unit's key tiles that lie in a stretch.
+struct UnitPart {
+  TokenTile t;
+  int sub;            // unit within the token tile: latent block, head chunk, column half
+  int kv;             // key tiles of the whole unit
+  int begin, end;     // key tiles in this stretch (begin < end, or the walk has ended)
+  bool valid;
+};
+// Walks the unit parts of a stretch in order. Each role walks on its own, one part ahead of the
+// one it works on, so the plan's reads are not waited for.
+struct UnitWalk {
+  const RowPlan* plan;
+  long long pos, hi;
+  int i, tiles, units, key_tile, causal;
+  __device__ __forceinline__ void init(const RowPlan* pl, const Stretch& s, int units_, int key_tile_, int causal_) {
+    plan = pl;
+    pos = s.lo;
+    hi = s.hi;
+    units = units_;
+    key_tile = key_tile_;
+    causal = causal_;
+    tiles = __ldg(pl->hdr);
+    int lo = 0, up = tiles;  // last tile with start <= pos (zero-cost tiles share a start: the last)
+    while (up - lo > 1) {
+      const int mid = (lo + up) >> 1;
+      if (__ldg(pl->start + mid) <= pos) lo = mid;
+      else up = mid;
+    }
+    i = lo;
+  }
+  __device__ __forceinline__ UnitPart next() {
+    UnitPart u;
+    u.valid = false;
+    u.begin = u.end = u.kv = u.sub = 0;
+    u.t = {0, 0, 0, 0};
+    while (pos < hi) {
+      const long long at = __ldg(plan->start + i), nx = __ldg(plan->start + i + 1);
+      if (pos >= nx) {
+        ++i;
+        continue;
+      }
+      const int4 raw = __ldg(reinterpret_cast<const int4*>(plan->tile + i));
+      u.t.b = raw.x; u.t.tok0 = raw.y; u.t.ntok = raw.z; u.t.lim0 = raw.w;
+      u.kv = key_tiles(u.t, causal, key_tile);
+      const int cost = unit_cost(u.kv);
+      u.sub = (int)((pos - at) / cost);
+      const long long first = at + (long long)u.sub * cost;
+      const long long b = pos - first - kUnitCost, e = hi - first - kUnitCost;
+      u.begin = b > 0 ? (int)b : 0;
+      u.end = e < u.kv ? (int)e : u.kv;
+      pos = first + cost;
+      if (u.end > u.begin) {
+        u.valid = true;
+        return u;
+      }
+    }
+    return u;
+  }
+};
+
+}  // namespace mlra

@@ -1,0 +1,946 @@
+// rows.cuh - attention of many query rows over paged latent rows (prompts, prompt chunks, shared
+// prefixes), in the absorbed form the decode step uses:
+//   S[r][t] = [q~ | q^R][r] . [c_j | k^R][t],  P = softmax over the keys row r may see,
+//   O[r]    = sum_t P[r][t] c_j[t]
+// A row r is one (query token, head) pair. Every head of a latent block reads the same cached rows,
+// so the rows of a token's heads are stacked in one MMA tile: with 32 heads a block (MLRA-4) a tile
+// of 128 rows is 4 tokens, and a prompt of any length fills its tiles to within 3 tokens. The key
+// tile is also the value tile (its first d_b columns), so each cached byte is staged once.
+//
+// Work is split along one line: a unit is a token tile of one latent block (and head chunk), a
+// unit's cost the key tiles it sees (plus a constant), and CTA c of the persistent grid takes the
+// stretch [c * quota, (c + 1) * quota) of all the units' costs laid end to end. A unit that lies in
+// one stretch is finished there; one that is cut leaves normalised fp32 partials with their
+// log-sum-exp, merged afterwards in a fixed order. The split needs lengths that only the device
+// has, so a one-CTA kernel (mlra_rows_plan_kernel) lays the units out.
+//
+// What bounds it: a 128 x 128 tile at d_b = 128, d_rope = 64 is 12 + 8 tcgen05 MMAs of 64 clocks
+// (1280) against 16384 exponentials (1024 clocks of the special-function units), so two row tiles
+// run in turn: one tile's softmax works while the other's MMAs run.
+#pragma once
+
+#include "common.cuh"
+#include "decode.cuh"
+#include "proj.cuh"
+#include "rowplan.cuh"
+
+namespace mlra {
+
+// D(tmem) (+)= A(tmem) * B(smem desc), bf16: A's row r lies in lane r, two K elements a column.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                            int w, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// ---------------------------------------------------------------------------------------
+// The attention kernel
+// ---------------------------------------------------------------------------------------
+// DB, DR: block and RoPE widths; KT: keys a tile (64 or 128); DV: value columns a CTA keeps
+// (DB, or a half of it where DB fp32 columns would fill the tensor memory); NQ row tiles in turn;
+// SB score buffers a row tile (NQ = 1 hides the softmax behind the next tile's scores instead).
+template <int DB_, int DR_, int KT_, int DV_, int NQ_, int STAGES_>
+struct RowShape {
+  static constexpr int DB = DB_, DR = DR_, KT = KT_, DV = DV_, NQ = NQ_, STAGES = STAGES_;
+  static constexpr int SB = NQ == 1 ? 2 : 1;
+  static constexpr int HALVES = DB / DV;
+  static constexpr int ROWS = 128 * NQ;     // query rows a unit
+  static constexpr int CW = DB < 64 ? DB : 64, NC = DB / CW, C_ROWB = CW * 2;
+  static constexpr int RW = DR < 64 ? DR : 64, NR = DR / RW, R_ROWB = RW * 2;
+  static constexpr int QC_REG = 128 * C_ROWB, QR_REG = 128 * R_ROWB;
+  static constexpr int Q_BYTES = NC * QC_REG + NR * QR_REG;
+  static constexpr int KC_REG = KT * C_ROWB, KR_REG = KT * R_ROWB;
+  static constexpr int STAGE_BYTES = NC * KC_REG + NR * KR_REG;
+  static constexpr int PAGE_TX = kPage * (DB + DR) * 2;
+  static constexpr int S_COL = 0;                       // NQ * SB buffers of KT columns
+  static constexpr int O_COL = NQ * SB * KT;
+  static constexpr int TMEM_USED = O_COL + NQ * DV;
+  static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
+  static constexpr int MMA_WARP = 4 * NQ, LOAD_WARP = MMA_WARP + 1, FIX_WARP = MMA_WARP + 2;
+  static constexpr int THREADS = 32 * (FIX_WARP + 1);
+  static constexpr int NBARS = 2 * STAGES + 2 + 2 * NQ * SB + 2 * NQ + 4;
+  static constexpr int OFF_STAGES = NQ * Q_BYTES;
+  static constexpr int OFF_BAR = OFF_STAGES + STAGES * STAGE_BYTES;
+  static constexpr int SMEM = OFF_BAR + NBARS * 8 + 64 + 1024;
+  static_assert(SMEM <= 227 * 1024 && TMEM_USED <= 512, "shared and tensor memory of one CTA");
+  static_assert(KT == 64 || KT == 128, "whole pages");
+  static_assert(DV <= 256 && DV % 16 == 0 && DB % DV == 0, "one PV instruction's columns");
+  static_assert(Q_BYTES % 1024 == 0 && STAGE_BYTES % 1024 == 0 && KC_REG % 1024 == 0 && QC_REG % 1024 == 0,
+                "swizzled regions start on 1024 bytes");
+};
+
+struct RowParams {
+  RowPlan plan;
+  const int* page_table;   // null: page i of sequence b is b * pt_stride + i
+  int pt_stride, num_pages;
+  int causal;
+  int nsub;                // (latent block, head chunk) pairs
+  int chunks;              // head chunks of a block
+  int heads_tile;          // heads of a row tile's tokens: min(heads of a block, np)
+  int tok_tile;            // tokens of a row tile: 128 / heads_tile
+  int heads_block, vh;     // heads of a block, (virtual) heads in all
+  int d_c;
+  float o_scale;           // value of a staged latent element (1, or the E4M3 cache's scale)
+  __nv_bfloat16* o_bf16;   // [tokens][vh][DB], or null
+  float* o_f32;            // [tokens][vh][DB] when o_bf16 is null
+  float* lse;              // [tokens][vh] or null: natural log beside o_bf16, log2 beside o_f32
+  float* part_o;           // [2 * CTAs][ROWS][DV]
+  float* part_lse;         // [2 * CTAs][ROWS] log2
+  int* status;
+  EarlyTags tags;
+  unsigned long long wait_limit_ns;
+};
+
+// A unit cut by the stretches leaves CTA c's part in slot 2c + 1 where the part begins the unit,
+// in slot 2c where it goes on with one begun before (a stretch holds at most one of each).
+template <class Sh>
+__global__ void __launch_bounds__(Sh::THREADS, 1)
+    mlra_rows_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_r,
+                     const __grid_constant__ CUtensorMap map_qc, const __grid_constant__ CUtensorMap map_qr,
+                     const RowParams p) {
+  constexpr int NQ = Sh::NQ, SB = Sh::SB, KT = Sh::KT, STAGES = Sh::STAGES, DV = Sh::DV;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* qbuf = smem;
+  uint8_t* stages = smem + Sh::OFF_STAGES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::OFF_BAR);
+  uint64_t* kfull = bars;
+  uint64_t* kempty = kfull + STAGES;
+  uint64_t* qfull = kempty + STAGES;
+  uint64_t* qempty = qfull + 1;
+  uint64_t* sfull = qempty + 1;          // [NQ * SB]
+  uint64_t* pfull = sfull + NQ * SB;     // [NQ * SB]
+  uint64_t* ofull = pfull + NQ * SB;     // [NQ]
+  uint64_t* ofree = ofull + NQ;          // [NQ]
+  uint64_t* pvdone = ofree + NQ;         // NQ = 1 only
+  uint64_t* patch = pvdone + 1;          // a key tile is ready to be patched
+  uint64_t* patched_bar = patch + 1;     // and has been
+  uint64_t* drained = patched_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Sh::NBARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* drain_err = abort_flag + 1;
+
+  const int warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 1);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    for (int s = 0; s < NQ * SB; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&pfull[s], 4);
+    }
+    for (int q = 0; q < NQ; ++q) {
+      mbar_init(&ofull[q], 1);
+      mbar_init(&ofree[q], 4);
+    }
+    mbar_init(pvdone, 1);
+    mbar_init(patch, 1);
+    mbar_init(patched_bar, 1);
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    *drain_err = 0;
+    fence_mbar_init();
+  }
+  if (warp == Sh::LOAD_WARP && lane == 0) {
+    tma_prefetch_map(&map_c);
+    tma_prefetch_map(&map_r);
+    tma_prefetch_map(&map_qc);
+    tma_prefetch_map(&map_qr);
+  }
+  // The plan, the packed query and the cleared status word come from kernels before this one. The
+  // tensor memory is taken after them too, so no CTA that waits holds what an earlier one needs.
+  grid_dependency_wait();
+  if (warp == Sh::MMA_WARP) {
+    tmem_alloc(tmem_slot, Sh::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  grid_launch_dependents();
+
+  const int units = p.nsub * Sh::HALVES;
+  const Stretch st = stretch_of(__ldg(p.plan.start + __ldg(p.plan.hdr)), blockIdx.x, gridDim.x);
+  UnitWalk walk;
+  walk.init(&p.plan, st, units, KT, p.causal);
+  UnitPart nx = walk.next();
+
+  uint32_t kt = 0;    // key tiles so far (stage ring)
+  uint32_t uc = 0;    // unit parts so far
+  uint32_t fc = 0;    // key tiles that were patched so far
+
+  if (warp == Sh::LOAD_WARP) {
+    // ------------------------------ TMA loads ------------------------------
+    const uint64_t pol = l2_policy_evict_last();
+    uint32_t issued = 0, parity = 0;
+    int q_parity = -1;  // of the last query load
+    bool ok = true;
+    while (nx.valid && ok) {
+      const UnitPart u = nx;
+      nx = walk.next();
+      const int sub = u.sub / Sh::HALVES;
+      const int blk = sub / p.chunks;
+      const int nrow = u.t.ntok > p.tok_tile ? NQ : 1;  // row tiles in use
+      if (lane == 0) {
+        ok = mbar_wait(qempty, (uc & 1) ^ 1, abort_flag, p.wait_limit_ns);
+        if (ok) {
+          const int rows = p.heads_tile * p.tok_tile;
+          mbar_arrive_expect_tx(qfull, nrow * rows * (Sh::DB + Sh::DR) * 2);
+          q_parity = uc & 1;
+          for (int q = 0; q < nrow; ++q) {
+            uint8_t* dst = qbuf + q * Sh::Q_BYTES;
+            const int tok = u.t.tok0 + q * p.tok_tile;
+            for (int r = 0; r < Sh::NC; ++r)
+              tma_load_4d(dst + r * Sh::QC_REG, &map_qc, qfull, r * Sh::CW, 0, sub, tok, pol);
+            for (int r = 0; r < Sh::NR; ++r)
+              tma_load_4d(dst + Sh::NC * Sh::QC_REG + r * Sh::QR_REG, &map_qr, qfull, Sh::DB + r * Sh::RW, 0, sub,
+                          tok, pol);
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      const int pages = (tile_limit(u.t, p.causal) + kPage - 1) / kPage;
+      const size_t row = (size_t)u.t.b * p.pt_stride;
+      constexpr int PPT = KT / kPage;  // pages a key tile
+      int wb = u.begin * PPT;
+      // page ids come through a window of two registers a lane, the next 32 read ahead
+      auto ids = [&](int base) {
+        const int pg = base + lane;
+        if (pg >= pages) return 0;
+        return p.page_table != nullptr ? __ldg(p.page_table + row + pg) : (int)row + pg;
+      };
+      int w0 = ids(wb), w1 = ids(wb + 32);
+      for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
+        const int p0 = t * PPT;
+        if (p0 >= wb + 32) {
+          wb += 32;
+          w0 = w1;
+          w1 = ids(wb + 32);
+        }
+        int id[PPT];
+#pragma unroll
+        for (int x = 0; x < PPT; ++x) id[x] = __shfl_sync(0xffffffffu, w0, (p0 + x - wb) & 31);
+        const int npg = min(PPT, pages - p0);
+        if (lane == 0) {
+          const int s = kt % STAGES;
+          const uint32_t ph = (kt / STAGES) & 1;
+          ok = mbar_wait(&kempty[s], ph ^ 1, abort_flag, p.wait_limit_ns);
+          if (ok) {
+            uint8_t* dst = stages + s * Sh::STAGE_BYTES;
+            mbar_arrive_expect_tx(&kfull[s], npg * Sh::PAGE_TX);
+            issued |= 1u << s;
+            parity = (parity & ~(1u << s)) | (ph << s);
+#pragma unroll
+            for (int x = 0; x < PPT; ++x) {
+              if (x >= npg) break;
+              if (id[x] < 0 || id[x] >= p.num_pages) {
+                set_status(p.status, kErrPageOob);
+                id[x] = 0;
+              }
+              const int y = id[x] * kPage;
+              for (int r = 0; r < Sh::NC; ++r)
+                tma_load_2d(dst + r * Sh::KC_REG + x * kPage * Sh::C_ROWB, &map_c, &kfull[s], blk * Sh::DB + r * Sh::CW,
+                            y, pol);
+              for (int r = 0; r < Sh::NR; ++r)
+                tma_load_2d(dst + Sh::NC * Sh::KC_REG + r * Sh::KR_REG + x * kPage * Sh::R_ROWB, &map_r, &kfull[s],
+                            p.d_c + r * Sh::RW, y, pol);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+      ++uc;
+    }
+    if (lane == 0) {
+      // nothing may still be landing when the CTA's shared memory is released
+      for (int s = 0; s < STAGES; ++s)
+        if ((issued >> s) & 1)
+          if (!mbar_wait_drain(&kfull[s], (parity >> s) & 1, p.wait_limit_ns)) *drain_err = 1;
+      if (q_parity >= 0 && !mbar_wait_drain(qfull, q_parity, p.wait_limit_ns)) *drain_err = 1;
+    }
+  } else if (warp == Sh::MMA_WARP) {
+    // ------------------------------ MMAs ------------------------------
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, KT, false, false);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV, false, true);
+      const uint32_t q_addr = smem_u32(qbuf), k_addr = smem_u32(stages);
+      auto issue_qk = [&](int q, uint32_t tile) {
+        const uint32_t a0 = q_addr + q * Sh::Q_BYTES, b0 = k_addr + (tile % STAGES) * Sh::STAGE_BYTES;
+        const uint32_t sbuf = q * SB + (SB == 2 ? tile & 1 : 0);
+        const uint32_t d = tbase + Sh::S_COL + sbuf * KT;
+#pragma unroll
+        for (int r = 0; r < Sh::NC; ++r)
+#pragma unroll
+          for (int ks = 0; ks < Sh::C_ROWB / 32; ++ks)
+            umma_bf16(d, smem_desc(a0 + r * Sh::QC_REG + ks * 32, 16, 8 * Sh::C_ROWB, swizzle_code(Sh::C_ROWB)),
+                      smem_desc(b0 + r * Sh::KC_REG + ks * 32, 16, 8 * Sh::C_ROWB, swizzle_code(Sh::C_ROWB)), idesc_qk,
+                      (r > 0 || ks > 0) ? 1u : 0u);
+#pragma unroll
+        for (int r = 0; r < Sh::NR; ++r)
+#pragma unroll
+          for (int ks = 0; ks < Sh::R_ROWB / 32; ++ks)
+            umma_bf16(d,
+                      smem_desc(a0 + Sh::NC * Sh::QC_REG + r * Sh::QR_REG + ks * 32, 16, 8 * Sh::R_ROWB,
+                                swizzle_code(Sh::R_ROWB)),
+                      smem_desc(b0 + Sh::NC * Sh::KC_REG + r * Sh::KR_REG + ks * 32, 16, 8 * Sh::R_ROWB,
+                                swizzle_code(Sh::R_ROWB)),
+                      idesc_qk, 1u);
+        umma_commit(&sfull[sbuf]);
+      };
+      auto issue_pv = [&](int q, uint32_t tile, int half, bool first) {
+        const uint32_t b0 = k_addr + (tile % STAGES) * Sh::STAGE_BYTES + half * (DV / Sh::CW) * Sh::KC_REG;
+        const uint32_t sbuf = q * SB + (SB == 2 ? tile & 1 : 0);
+        const uint32_t a = tbase + Sh::S_COL + sbuf * KT;
+#pragma unroll
+        for (int ks = 0; ks < KT / 16; ++ks)
+          umma_bf16_ts(tbase + Sh::O_COL + q * DV, a + ks * 8,
+                       smem_desc(b0 + ks * 16 * Sh::C_ROWB, Sh::KC_REG, 8 * Sh::C_ROWB, swizzle_code(Sh::C_ROWB)),
+                       idesc_pv, (first && ks == 0) ? 0u : 1u);
+      };
+      auto wait = [&](uint64_t* b, uint32_t par) { return mbar_wait(b, par, abort_flag, p.wait_limit_ns); };
+      uint32_t pc[NQ];  // score tiles so far, a row tile
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) pc[q] = 0;
+      uint32_t oc[NQ];  // parts so far, a row tile
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) oc[q] = 0;
+      bool ok = true;
+      while (nx.valid && ok) {
+        const UnitPart u = nx;
+        nx = walk.next();
+        const int half = u.sub % Sh::HALVES;
+        const int nrow = NQ == 2 && u.t.ntok > p.tok_tile ? 2 : 1;
+        const int n = u.end - u.begin;
+        ok = wait(qfull, uc & 1) && wait(&kfull[kt % STAGES], (kt / STAGES) & 1);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+          if (q < nrow) issue_qk(q, kt);
+        // a tile that reaches past what the unit's first token sees is patched (see the patch
+        // warp) between its score MMAs and its value MMAs
+        auto patched = [&](int i) { return (u.begin + i + 1) * KT > u.t.lim0; };
+        if (patched(0)) umma_commit(patch);
+        if (n == 1) umma_commit(qempty);
+        // the next tile's scores go out before this tile's values where a second stage holds it
+        auto next_qk = [&](int i) {
+          if (i + 1 >= n) return true;
+          const uint32_t tile = kt + i + 1;
+          if (!wait(&kfull[tile % STAGES], (tile / STAGES) & 1)) return false;
+          tc_fence_after();
+          issue_qk(0, tile);
+          if (patched(i + 1)) umma_commit(patch);
+          if (i + 2 == n) umma_commit(qempty);
+          return true;
+        };
+        for (int i = 0; i < n && ok; ++i) {
+          const uint32_t tile = kt + i;
+          if (NQ == 1 && STAGES > 1) ok = next_qk(i);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if (q >= nrow || !ok) break;
+            const uint32_t pb = q * SB + (SB == 2 ? tile & 1 : 0);
+            const uint32_t pph = SB == 2 ? (tile >> 1) & 1 : pc[q] & 1;
+            ok = wait(&pfull[pb], pph);
+            if (ok && q == 0 && patched(i)) ok = wait(patched_bar, fc & 1);
+            if (ok && i == 0) ok = wait(&ofree[q], (oc[q] & 1) ^ 1);
+            if (!ok) break;
+            ++pc[q];
+            tc_fence_after();
+            issue_pv(q, tile, half, i == 0);
+            if (q == nrow - 1) umma_commit(&kempty[tile % STAGES]);
+            if (NQ == 1) umma_commit(pvdone);
+            if (i == n - 1) {
+              umma_commit(&ofull[q]);
+              ++oc[q];
+            }
+            if (NQ == 2 && i + 1 < n) {
+              if (q == 0) {
+                ok = wait(&kfull[(tile + 1) % STAGES], ((tile + 1) / STAGES) & 1);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              issue_qk(q, tile + 1);
+              if (q == nrow - 1) {
+                if (patched(i + 1)) umma_commit(patch);
+                if (i + 2 == n) umma_commit(qempty);
+              }
+            }
+          }
+          if (patched(i)) ++fc;
+          if (NQ == 1 && STAGES == 1 && ok) ok = next_qk(i);
+        }
+        kt += n;
+        ++uc;
+      }
+      umma_commit(drained);
+      if (!mbar_wait_drain(drained, 0, p.wait_limit_ns)) *drain_err = 1;
+    }
+    __syncwarp();
+  } else if (warp == Sh::FIX_WARP) {
+    // ------------------------------ patches ------------------------------
+    // A masked key has P = 0, but 0 x NaN is NaN: where a key tile reaches past what the unit's
+    // first token sees, the value rows no token of the unit sees are zeroed (they may lie past the
+    // sequence's end, where a slot may hold anything), and elements of the rows that only some of
+    // its tokens see are zeroed where they are not finite. A token that does see such a row gets
+    // its NaN through the score, whose MMA has read the tile before it is patched.
+    bool ok = true;
+    while (nx.valid && ok) {
+      const UnitPart u = nx;
+      nx = walk.next();
+      const int lim = tile_limit(u.t, p.causal);
+      for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
+        if ((t + 1) * KT > u.t.lim0) {
+          // the MMAs that form this key tile's scores have read it (and it had landed)
+          ok = mbar_wait(patch, fc & 1, abort_flag, p.wait_limit_ns) &&
+               mbar_wait(&kfull[kt % STAGES], (kt / STAGES) & 1, abort_flag, p.wait_limit_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++fc;
+          uint8_t* st_mem = stages + (kt % STAGES) * Sh::STAGE_BYTES;
+          const int k0 = t * KT;
+          const int some = max(0, min(KT, max(u.t.lim0, 0) - k0));  // rows [some, none) only some tokens see
+          const int none = max(0, min(KT, lim - k0));
+          constexpr int CPR = Sh::C_ROWB / 16;
+          for (int r = 0; r < Sh::NC; ++r) {
+            uint8_t* reg = st_mem + r * Sh::KC_REG;
+            for (int i = none * CPR + lane; i < KT * CPR; i += 32)
+              *reinterpret_cast<uint4*>(reg + i * 16) = make_uint4(0, 0, 0, 0);
+            for (int i = some * CPR + lane; i < none * CPR; i += 32) {
+              uint4 v = *reinterpret_cast<const uint4*>(reg + i * 16);
+              uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+              bool hit = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; hit = true; }
+                if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0x0000ffffu; hit = true; }
+              }
+              if (hit) *reinterpret_cast<uint4*>(reg + i * 16) = v;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(patched_bar);
+        }
+      }
+    }
+  } else {
+    // ------------------------------ softmax and results ------------------------------
+    // A thread owns one row. The running maximum is raised only when a score passes it by more
+    // than 8 (log2 units), so P stays below 2^8 and O is rescaled in tensor memory only then.
+    const int q = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int tl = row / p.heads_tile;                     // token within the row tile
+    const int hr = row - tl * p.heads_tile;                // head within the tile's heads
+    const int tok = q * p.tok_tile + tl;                   // token within the unit
+    const bool row_in = tl < p.tok_tile;
+    uint32_t sc = 0, oc = 0;
+    bool ok = true;
+    while (nx.valid && ok) {
+      const UnitPart u = nx;
+      nx = walk.next();
+      const int n = u.end - u.begin;
+      if (q > 0 && u.t.ntok <= p.tok_tile) {
+        kt += n;
+        continue;
+      }
+      const int lim = p.causal ? u.t.lim0 + tok : u.t.lim0;  // keys this row sees
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < n; ++i, ++kt, ++sc) {
+        const uint32_t sb = q * SB + (SB == 2 ? kt & 1 : 0);
+        const uint32_t par = SB == 2 ? (kt >> 1) & 1 : sc & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[sb], par, abort_flag, p.wait_limit_ns));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t s_addr = tbase + lane_base + Sh::S_COL + sb * KT;
+        float s[KT];
+        tmem_load_row<KT>(s_addr, s);
+        tmem_ld_wait();
+        const int k0 = (u.begin + i) * KT;
+        if (k0 + KT > u.t.lim0) {
+#pragma unroll
+          for (int c = 0; c < KT; ++c) s[c] = k0 + c < lim ? s[c] : -INFINITY;
+        }
+        float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+#pragma unroll
+        for (int c = 4; c < KT; c += 4) {
+          x0 = fmaxf(x0, s[c]);
+          x1 = fmaxf(x1, s[c + 1]);
+          x2 = fmaxf(x2, s[c + 2]);
+          x3 = fmaxf(x3, s[c + 3]);
+        }
+        const float mt = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+        if (i == 0) {
+          m = mt;
+        } else {
+          const bool raise = mt > m + 8.f;
+          if (__any_sync(0xffffffffu, raise)) {
+            // with one score buffer this tile's scores were issued after the last PV; with two the
+            // last PV has its own barrier
+            // (waited for from the phase before it, so that the parity is that phase's)
+            if (NQ == 1) {
+              ok = kt < 2 || mbar_wait(pvdone, kt & 1, abort_flag, p.wait_limit_ns);
+              ok = ok && mbar_wait(pvdone, (kt - 1) & 1, abort_flag, p.wait_limit_ns);
+              ok = __all_sync(0xffffffffu, ok);
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const float a = raise ? fast_exp2(m - mt) : 1.f;
+            l *= a;
+            if (raise) m = mt;
+#pragma unroll 1
+            for (int c = 0; c < DV; c += 32) {
+              float o[32];
+              tmem_load_row<32>(tbase + lane_base + Sh::O_COL + q * DV + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= a;
+              tmem_store_row<32>(tbase + lane_base + Sh::O_COL + q * DV + c, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float mu = m == -INFINITY ? 0.f : m;  // a row that sees no key of this part: P = 0
+        float l0 = 0.f, l1 = 0.f;
+        uint32_t pk[KT / 2];
+#pragma unroll
+        for (int c = 0; c < KT; c += 2) {
+          float e0, e1;
+          sub_f32x2(e0, e1, s[c], s[c + 1], mu, mu);
+          e0 = fast_exp2(e0);
+          e1 = fast_exp2(e1);
+          add_f32x2(l0, l1, l0, l1, e0, e1);
+          pk[c / 2] = pack_bf16x2(e0, e1);  // P to bf16 (half a step 2^-9) for the tensor core
+        }
+        l += l0 + l1;
+#pragma unroll
+        for (int c = 0; c < KT / 2; c += 32) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = pk[c + e];
+          tmem_st32(s_addr + c, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[sb]);
+      }
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(&ofull[q], oc & 1, abort_flag, p.wait_limit_ns));
+      if (!ok) break;
+      ++oc;
+      tc_fence_after();
+      // ---- results of this part ----
+      const int half = u.sub % Sh::HALVES, sub = u.sub / Sh::HALVES;
+      const int head = (sub / p.chunks) * p.heads_block + (sub % p.chunks) * p.heads_tile + hr;
+      const bool mine = row_in && tok < u.t.ntok;
+      const bool whole = u.begin == 0 && u.end == u.kv;
+      const int slot = 2 * blockIdx.x + (u.begin == 0 ? 1 : 0);
+      const float inv = l > 0.f ? p.o_scale / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
+      const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
+      const size_t at = (size_t)(u.t.tok0 + tok) * p.vh + head;
+      const size_t pat = (size_t)slot * Sh::ROWS + q * 128 + row;
+      if (mine && half == 0) {
+        if (!whole)
+          p.part_lse[pat] = lse2;
+        else if (p.lse != nullptr)
+          p.lse[at] = p.o_bf16 != nullptr ? lse2 * kLn2 : lse2;
+      }
+      if (mine && half != 0 && !whole) p.part_lse[pat] = lse2;
+#pragma unroll 1
+      for (int c = 0; c < DV; c += 32) {
+        float o[32];
+        tmem_load_row<32>(tbase + lane_base + Sh::O_COL + q * DV + c, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= inv;
+        if (mine && whole && p.o_bf16 != nullptr) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o_bf16 + at * Sh::DB + half * DV + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+        } else if (mine) {
+          float4* dst = reinterpret_cast<float4*>(whole ? p.o_f32 + at * Sh::DB + half * DV + c : p.part_o + pat * DV + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ofree[q]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (blockIdx.x == 0) fold_early(p.tags, p.status);
+    if (*abort_flag) set_status(p.status, kErrTimeout);
+    if (*drain_err) force_status(p.status, kErrDrain);
+  }
+  if (warp == Sh::MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tbase, Sh::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Merge of the units that the stretches cut (and zeros for tokens that see no key)
+// ---------------------------------------------------------------------------------------
+struct MergeParams {
+  RowPlan plan;
+  int ctas;                // grid of the attention kernel
+  int causal, key_tile, units, halves, nsub, chunks, heads_tile, tok_tile, heads_block, vh, db, dv, rows;
+  const float* part_o;
+  const float* part_lse;
+  __nv_bfloat16* o_bf16;   // [tokens][vh][db]
+  float* lse;              // natural log, or null
+};
+
+// Grid (ctas, row slices). Block (c, s) looks after the boundary at the start of CTA c's stretch: if it
+// is the first boundary inside a unit, the unit's parts (CTAs c - 1, c, ... in that order) are
+// merged by log-sum-exp. A warp takes a row, a lane dv / 32 features.
+__global__ void __launch_bounds__(256) mlra_rows_merge_kernel(const MergeParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int tiles = __ldg(p.plan.hdr);
+  const long long total = __ldg(p.plan.start + tiles);
+  const int warp = warp_id(), lane = lane_id(), nwarp = blockDim.x >> 5;
+  const int slice = blockIdx.y * nwarp + warp, slices = gridDim.y * nwarp;
+  // token tiles without a key: zeros
+  for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
+    const TokenTile t = p.plan.tile[i];
+    if (key_tiles(t, p.causal, p.key_tile) > 0) continue;
+    for (long long r = slice; r < (long long)t.ntok * p.vh; r += slices) {
+      const size_t at = (size_t)t.tok0 * p.vh + r;
+      for (int f = lane * 2; f < p.db; f += 64) *reinterpret_cast<uint32_t*>(p.o_bf16 + at * p.db + f) = 0u;
+      if (lane == 0 && p.lse != nullptr) p.lse[at] = -INFINITY;
+    }
+  }
+  const int c = blockIdx.x;
+  const Stretch st = stretch_of(total, c, p.ctas);
+  if (c == 0 || st.lo >= total) return;
+  int lo = 0, up = tiles;  // the tile that holds position st.lo
+  while (up - lo > 1) {
+    const int mid = (lo + up) >> 1;
+    if (__ldg(p.plan.start + mid) <= st.lo) lo = mid;
+    else up = mid;
+  }
+  const TokenTile t = p.plan.tile[lo];
+  const int kv = key_tiles(t, p.causal, p.key_tile);
+  const int cost = unit_cost(kv);
+  const long long at0 = __ldg(p.plan.start + lo);
+  const int usub = (int)((st.lo - at0) / cost);
+  const long long first = at0 + (long long)usub * cost + kUnitCost, last = first + kv - 1;  // its key tiles
+  if (st.lo <= first || st.lo > last) return;  // the boundary does not cut the unit's key tiles
+  const int c0 = (int)(first / st.quota), c1 = (int)(last / st.quota);
+  if (c0 != c - 1) return;                     // not the first boundary in it
+  const int sub = usub / p.halves, half = usub % p.halves;
+  const int per = p.dv / 32;
+  for (int r = slice; r < p.rows; r += slices) {
+    const int q = r >> 7, row = r & 127;
+    const int tl = row / p.heads_tile, hr = row - tl * p.heads_tile;
+    const int tok = q * p.tok_tile + tl;
+    if (tl >= p.tok_tile || tok >= t.ntok) continue;
+    float mx = -INFINITY, sum = 0.f;
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int x = c0; x <= c1; ++x) {
+      const size_t at = (size_t)(2 * x + (x == c0 ? 1 : 0)) * p.rows + r;
+      const float lv = __ldg(p.part_lse + at);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < per ? __ldg(p.part_o + at * p.dv + e * 32 + lane) : 0.f;
+      if (lv == -INFINITY) continue;
+      const float mn = fmaxf(mx, lv);
+      const float a = fast_exp2(mx - mn), w = fast_exp2(lv - mn);
+      sum = sum * a + w;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + w * v[e];
+      mx = mn;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int head = (sub / p.chunks) * p.heads_block + (sub % p.chunks) * p.heads_tile + hr;
+    const size_t at = (size_t)(t.tok0 + tok) * p.vh + head;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < per) p.o_bf16[at * p.db + half * p.dv + e * 32 + lane] = __float2bfloat16_rn(acc[e] * inv);
+    if (lane == 0 && half == 0 && p.lse != nullptr)
+      p.lse[at] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Up-projection of many tokens: out[t][h] = out_scale * W^UV_h o~[t][h]
+// ---------------------------------------------------------------------------------------
+// A persistent grid over (head, tile of 128 tokens) in head-major order, each CTA a contiguous run, so
+// a CTA keeps one head's weight in shared memory for most of its run. M = 128 tokens, N = d_h,
+// K = SUMK * d_b (summed blocks: the blocks' latents and weights stacked along K); A tiles of 64
+// columns come through a ring, two accumulators alternate. Bound by memory: it reads o~ and writes
+// out once, 512 bytes for 2 * 128 * 128 FLOPs.
+template <int DBB_, int DH_, int SUMK_>
+struct UpShape {
+  static constexpr int DBB = DBB_, DH = DH_, SUMK = SUMK_, K = DBB * SUMK;
+  static constexpr int CW = DBB < 64 ? DBB : 64, ROWB = CW * 2, NKC = K / CW;
+  static constexpr int AW = DH < 64 ? DH : 64, WROWB = AW * 2, NATOM = DH / AW;
+  static constexpr int ATOM = K * WROWB;
+  static constexpr int W_BYTES = NATOM * ATOM;
+  static constexpr int A_REG = 128 * ROWB;
+  static constexpr int STAGES = 4;
+  static constexpr int WBOX = DBB < 256 ? DBB : 256;  // rows of the weight map's box
+  static constexpr int TMEM_COLS = 2 * DH < 32 ? 32 : 2 * DH;
+  static constexpr int OFF_RING = W_BYTES;
+  static constexpr int OFF_BAR = OFF_RING + STAGES * A_REG;
+  static constexpr int SMEM = OFF_BAR + (2 * STAGES + 2 + 4 + 1) * 8 + 64 + 1024;
+  static constexpr int THREADS = 192;
+  static_assert(W_BYTES % 1024 == 0 && A_REG % 1024 == 0 && SMEM <= 227 * 1024, "layout");
+};
+
+struct UpParams {
+  const int* used;       // tokens in use (rows past them are left as they were)
+  void* out;             // [tokens][heads][DH]
+  int out_f32, heads;
+  float out_scale;
+  int* status;
+  unsigned long long wait_limit_ns;
+};
+
+template <class Sh>
+__global__ void __launch_bounds__(Sh::THREADS)
+    mlra_rows_up_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_o,
+                        const UpParams p) {
+  constexpr int DH = Sh::DH, STAGES = Sh::STAGES, NKC = Sh::NKC;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* wbuf = smem;
+  uint8_t* ring = smem + Sh::OFF_RING;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Sh::OFF_BAR);
+  uint64_t* empty = full + STAGES;
+  uint64_t* wfull = empty + STAGES;
+  uint64_t* wfree = wfull + 1;
+  uint64_t* dfull = wfree + 1;   // [2]
+  uint64_t* dfree = dfull + 2;   // [2]
+  uint64_t* drained = dfree + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* drain_err = abort_flag + 1;
+  const int warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(wfull, 1);
+    mbar_init(wfree, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&dfull[i], 1);
+      mbar_init(&dfree[i], 4);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    *drain_err = 0;
+    fence_mbar_init();
+  }
+  grid_dependency_wait();
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, Sh::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  grid_launch_dependents();
+
+  const int used = __ldg(p.used);
+  const int tiles = (used + 127) / 128;
+  const long long items = (long long)tiles * p.heads;
+  const long long per = (items + gridDim.x - 1) / gridDim.x;
+  const long long lo = min(per * blockIdx.x, items), hi = min(lo + per, items);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_first(), keep = l2_policy_evict_last();
+      uint32_t c = 0, wc = 0, issued = 0, parity = 0;
+      int w_parity = -1, head = -1;
+      bool ok = true;
+      for (long long it = lo; it < hi && ok; ++it) {
+        const int h = (int)(it / tiles), tok = (int)(it % tiles) * 128;
+        if (h != head) {
+          head = h;
+          ok = mbar_wait(wfree, (wc & 1) ^ 1, abort_flag, p.wait_limit_ns);
+          if (!ok) break;
+          mbar_arrive_expect_tx(wfull, Sh::W_BYTES);
+          w_parity = wc & 1;
+          for (int a = 0; a < Sh::NATOM; ++a)
+            for (int j = 0; j < Sh::SUMK; ++j)
+              for (int r = 0; r < Sh::DBB; r += Sh::WBOX)
+                tma_load_2d(wbuf + a * Sh::ATOM + (j * Sh::DBB + r) * Sh::WROWB, &map_w, wfull, a * Sh::AW,
+                            (j * p.heads + h) * Sh::DBB + r, keep);
+          ++wc;
+        }
+        for (int kc = 0; kc < NKC && ok; ++kc, ++c) {
+          const int s = c % STAGES;
+          const uint32_t ph = (c / STAGES) & 1;
+          ok = mbar_wait(&empty[s], ph ^ 1, abort_flag, p.wait_limit_ns);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&full[s], Sh::A_REG);
+          issued |= 1u << s;
+          parity = (parity & ~(1u << s)) | (ph << s);
+          const int f = kc * Sh::CW;
+          tma_load_3d(ring + s * Sh::A_REG, &map_o, &full[s], f % Sh::DBB, (f / Sh::DBB) * p.heads + h, tok, pol);
+        }
+      }
+      for (int s = 0; s < STAGES; ++s)
+        if ((issued >> s) & 1)
+          if (!mbar_wait_drain(&full[s], (parity >> s) & 1, p.wait_limit_ns)) *drain_err = 1;
+      if (w_parity >= 0 && !mbar_wait_drain(wfull, w_parity, p.wait_limit_ns)) *drain_err = 1;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, DH, false, true);
+      const uint32_t w0 = smem_u32(wbuf), a0 = smem_u32(ring);
+      uint32_t c = 0, wc = 0, n = 0;
+      int head = -1;
+      bool ok = true;
+      for (long long it = lo; it < hi && ok; ++it, ++n) {
+        const int h = (int)(it / tiles);
+        if (h != head) {
+          head = h;
+          ok = mbar_wait(wfull, wc & 1, abort_flag, p.wait_limit_ns);
+          if (!ok) break;
+          ++wc;
+        }
+        const uint32_t d = tbase + (n & 1) * DH;
+        ok = mbar_wait(&dfree[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, p.wait_limit_ns);
+        for (int kc = 0; kc < NKC && ok; ++kc, ++c) {
+          const int s = c % STAGES;
+          ok = mbar_wait(&full[s], (c / STAGES) & 1, abort_flag, p.wait_limit_ns);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < Sh::ROWB / 32; ++ks)
+            umma_bf16(d, smem_desc(a0 + s * Sh::A_REG + ks * 32, 16, 8 * Sh::ROWB, swizzle_code(Sh::ROWB)),
+                      smem_desc(w0 + (kc * Sh::CW + ks * 16) * Sh::WROWB, Sh::ATOM, 8 * Sh::WROWB,
+                                swizzle_code(Sh::WROWB)),
+                      idesc, (kc > 0 || ks > 0) ? 1u : 0u);
+          umma_commit(&empty[s]);
+        }
+        if (!ok) break;
+        umma_commit(&dfull[n & 1]);
+        if (it + 1 < hi && (int)((it + 1) / tiles) != head) umma_commit(wfree);
+      }
+      umma_commit(drained);
+      if (!mbar_wait_drain(drained, 0, p.wait_limit_ns)) *drain_err = 1;
+    }
+    __syncwarp();
+  } else {
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint32_t n = 0;
+    for (long long it = lo; it < hi; ++it, ++n) {
+      const int h = (int)(it / tiles), tok = (int)(it % tiles) * 128 + row;
+      if (!__all_sync(0xffffffffu, mbar_wait(&dfull[n & 1], (n >> 1) & 1, abort_flag, p.wait_limit_ns))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < DH; c += 32) {
+        float v[32];
+        tmem_load_row<32>(tbase + lane_base + (n & 1) * DH + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] *= p.out_scale;
+        const size_t at = ((size_t)tok * p.heads + h) * DH + c;
+        if (tok >= used) {
+          // rows behind the last sequence stay as they were
+        } else if (p.out_f32) {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dfree[n & 1]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (*abort_flag) set_status(p.status, kErrTimeout);
+    if (*drain_err) force_status(p.status, kErrDrain);
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, Sh::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// E4M3 cache: the sequences' pages as bf16 pages
+// ---------------------------------------------------------------------------------------
+// One block a page: page i of sequence b becomes page b * pt_stride + i of `dst`. Every E4M3 value is a
+// bf16 value, so nothing is rounded; the cache's scales are applied to the query and the result.
+// Reads 576 and writes 1152 bytes a token at d_c = 512, once a call, against 640 * heads FLOPs a
+// query token and cached token.
+__global__ void __launch_bounds__(256) mlra_widen_pages_kernel(const uint8_t* __restrict__ pool, int num_pages,
+                                                               const int* __restrict__ page_table, int pt_stride,
+                                                               const int* __restrict__ lens, int width,
+                                                               __nv_bfloat16* __restrict__ dst, int* status) {
+  grid_dependency_wait();  // the buffer may be in use by the work before, and the status word is cleared there
+  grid_launch_dependents();
+  const int b = blockIdx.y, i = blockIdx.x;
+  int n = __ldg(lens + b);
+  n = n < 0 ? 0 : n > pt_stride * kPage ? pt_stride * kPage : n;
+  if (i * kPage >= n) return;
+  int id = __ldg(page_table + (size_t)b * pt_stride + i);
+  if (id < 0 || id >= num_pages) {
+    if (threadIdx.x == 0) set_status(status, kErrPageOob);
+    id = 0;
+  }
+  const uint4* src = reinterpret_cast<const uint4*>(pool + (size_t)id * kPage * width);
+  uint4* out = reinterpret_cast<uint4*>(dst + ((size_t)b * pt_stride + i) * kPage * width);
+  for (int x = threadIdx.x; x < kPage * width / 16; x += blockDim.x) {
+    const uint4 v = __ldg(src + x);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t h2 = f16x2_from_e4m3x2(static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1))));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+      o[e] = pack_bf16x2(f.x, f.y);
+    }
+    out[2 * x] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[2 * x + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+}  // namespace mlra

@@ -1,0 +1,537 @@
+// rows_api.cuh - host side of mlra_prefill and mlra_decode_prefix (included by mlra_api.cu, whose
+// handle, tensor maps and launch helpers it uses): argument checks, workspace, launch sequence.
+#pragma once
+
+namespace {
+
+// Shapes of the row attention, one a set of block dims. MLRA-4 blocks (d_b = 128) run two row tiles in
+// turn; at d_b = 256 a row tile's O fills half the tensor memory, so one row tile alternates two
+// score buffers over 64-key tiles; at d_b = 512 two CTAs keep a half of O each and both form the
+// scores (64 % of their MMA work is then O(1) repeated, but no exchange between SMs is needed).
+using RowsTiny = RowShape<32, 16, 128, 32, 2, 4>;
+using RowsB128 = RowShape<128, 64, 128, 128, 2, 2>;
+using RowsB256 = RowShape<256, 64, 64, 256, 1, 3>;
+using RowsB512 = RowShape<512, 64, 64, 256, 1, 1>;
+
+constexpr int kMaxQueryTokens = 1 << 21;  // grid rows of the absorb kernel
+
+template <class F>
+auto with_rows(Variant v, F f) {
+  switch (v) {
+    case kTiny: return f(RowsTiny{});
+    case kMlra2: case kMlra2Sum: return f(RowsB256{});
+    case kMla: return f(RowsB512{});
+    default: return f(RowsB128{});
+  }
+}
+
+template <int DBB, int DH, int SUMK>
+cudaError_t prep_up() {
+  return prep_kernel(mlra_rows_up_kernel<UpShape<DBB, DH, SUMK>>, UpShape<DBB, DH, SUMK>::SMEM);
+}
+cudaError_t prep_rows(Variant v) {
+  cudaError_t e = with_rows(v, [](auto sh) {
+    using Sh = decltype(sh);
+    return prep_kernel(mlra_rows_kernel<Sh>, Sh::SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  switch (v) {
+    case kTiny:
+      e = prep_up<32, 32, 1>();
+      return e == cudaSuccess ? prep_up<32, 32, 4>() : e;
+    case kMlra2: return prep_up<256, 128, 1>();
+    case kMlra2Sum: return prep_up<256, 128, 2>();
+    case kMla: return prep_up<512, 128, 1>();
+    case kMlra4Sum: return prep_up<128, 128, 4>();
+    default: return prep_up<128, 128, 1>();
+  }
+}
+
+// The combine with prefix parts (the decode step's combine kernel, one more template flag).
+template <int DB, int DH, int SUMK, int NT>
+cudaError_t prep_prefix_nt() {
+  using S = ProjShape<DB, DH, NT>;
+  return prep_kernel(mlra_uproj_kernel<S, false, SUMK, true>, S::SMEM4);
+}
+template <int DB, int DH, int SUMK>
+cudaError_t prep_prefix_proj() {
+  cudaError_t e = prep_prefix_nt<DB, DH, SUMK, 16>();
+  if (e == cudaSuccess) e = prep_prefix_nt<DB, DH, SUMK, 32>();
+  if (e == cudaSuccess) e = prep_prefix_nt<DB, DH, SUMK, 64>();
+  if constexpr (max_nt<DB>() >= 128)
+    if (e == cudaSuccess) e = prep_prefix_nt<DB, DH, SUMK, 128>();
+  return e;
+}
+cudaError_t prep_prefix(Variant v, bool summed) {
+  switch (v) {
+    case kTiny: return summed ? prep_prefix_proj<128, 32, 4>() : prep_prefix_proj<32, 32, 1>();
+    case kMlra4: return prep_prefix_proj<128, 128, 1>();
+    case kMlra4Sum: return prep_prefix_proj<512, 128, 4>();
+    case kMlra2: return prep_prefix_proj<256, 128, 1>();
+    case kMlra2Sum: return prep_prefix_proj<512, 128, 2>();
+    case kMla: return prep_prefix_proj<512, 128, 1>();
+    default: return cudaSuccess;  // E4M3 cache: no shared-prefix decode
+  }
+}
+
+template <int DB, int DH, int SUMK, int NT>
+cudaError_t launch_uproj_prefix(const mlra_ctx* h, const ProjParams& pp, int batch, cudaStream_t s) {
+  using S = ProjShape<DB, DH, NT>;
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t c =
+      launch_cfg(dim3(h->cfg.h, (batch + NT - 1) / NT), dim3(kProjThreads), S::SMEM4, s, true, &attr);
+  return cudaLaunchKernelEx(&c, mlra_uproj_kernel<S, false, SUMK, true>, h->map_wuv, pp);
+}
+template <int DB, int DH, int SUMK>
+cudaError_t dispatch_uproj_prefix(const mlra_ctx* h, const ProjParams& pp, int batch, cudaStream_t s) {
+  switch (nt_for(batch, max_nt<DB>())) {
+    case 16: return launch_uproj_prefix<DB, DH, SUMK, 16>(h, pp, batch, s);
+    case 32: return launch_uproj_prefix<DB, DH, SUMK, 32>(h, pp, batch, s);
+    case 64: return launch_uproj_prefix<DB, DH, SUMK, 64>(h, pp, batch, s);
+    default:
+      if constexpr (max_nt<DB>() >= 128) return launch_uproj_prefix<DB, DH, SUMK, 128>(h, pp, batch, s);
+      return cudaErrorInvalidValue;
+  }
+}
+
+// A bump allocator over the caller's workspace (base null: sizes only).
+struct Carver {
+  char* base;
+  size_t off;
+  template <class T>
+  T* take(size_t count) {
+    T* p = reinterpret_cast<T*>(base + off);
+    off += align256(count * sizeof(T));
+    return p;
+  }
+};
+
+struct RowsWorkspace {
+  RowPlan plan;
+  float* part_o;
+  float* part_lse;
+};
+// Plan and partial slots of the row attention over `tokens` query tokens of `seqs` sequences.
+RowsWorkspace carve_rows(const mlra_ctx* h, Carver& c, size_t tokens, size_t seqs, bool tok_tile) {
+  return with_rows(h->var, [&](auto sh) {
+    using Sh = decltype(sh);
+    const int heads = h->heads_block < h->np ? h->heads_block : h->np;
+    const size_t tile = (size_t)Sh::NQ * (128 / heads);
+    const size_t tiles = tokens / tile + seqs;
+    RowsWorkspace w;
+    w.plan.hdr = c.take<int>(4);
+    w.plan.start = c.take<long long>(tiles + 1);
+    w.plan.tile = c.take<TokenTile>(tiles);
+    w.plan.tok_tile = tok_tile ? c.take<int>(tokens) : nullptr;
+    w.part_lse = c.take<float>((size_t)2 * h->num_sms * Sh::ROWS);
+    w.part_o = c.take<float>((size_t)2 * h->num_sms * Sh::ROWS * Sh::DV);
+    return w;
+  });
+}
+
+struct PrefillWorkspace {
+  int* status;
+  __nv_bfloat16* q_pack;
+  __nv_bfloat16* o;
+  __nv_bfloat16* pages;  // E4M3 cache only
+  RowsWorkspace rows;
+  size_t bytes;
+};
+PrefillWorkspace carve_prefill(const mlra_ctx* h, int total_q, int batch, int pt_stride, void* base) {
+  Carver c = {static_cast<char*>(base), 0};
+  PrefillWorkspace w;
+  w.status = c.take<int>(64);
+  w.q_pack = c.take<__nv_bfloat16>((size_t)total_q * h->nsub * h->np * (h->d_b + h->d_r));
+  w.o = c.take<__nv_bfloat16>((size_t)total_q * h->vh * h->d_b);
+  w.rows = carve_rows(h, c, total_q, batch, false);
+  w.pages = h->fp8 ? c.take<__nv_bfloat16>((size_t)batch * pt_stride * kPage * (h->cfg.d_c + h->d_r)) : nullptr;
+  w.bytes = c.off;
+  return w;
+}
+
+struct PrefixWorkspace {
+  Workspace dec;       // of the decode step over the sequences' own rows (at the workspace's start)
+  float* o;            // [batch][vh][d_b]
+  float* lse;          // [batch][vh]
+  RowsWorkspace rows;
+  size_t bytes;
+};
+PrefixWorkspace carve_prefix(const mlra_ctx* h, int batch, int groups, void* base) {
+  PrefixWorkspace w;
+  w.dec = carve(h, batch, base);
+  Carver c = {static_cast<char*>(base), w.dec.bytes};
+  w.o = c.take<float>((size_t)batch * h->vh * h->d_b);
+  w.lse = c.take<float>((size_t)batch * h->vh);
+  w.rows = carve_rows(h, c, batch, groups, true);
+  w.bytes = c.off;
+  return w;
+}
+
+bool make_qpack_map(CUtensorMap* m, const mlra_ctx* h, const void* q_pack, uint64_t tokens, uint32_t box_cols,
+                    uint32_t heads, uint32_t box_tokens) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  const uint64_t row = (uint64_t)(h->d_b + h->d_r) * 2;
+  cuuint64_t dims[4] = {(cuuint64_t)(h->d_b + h->d_r), (cuuint64_t)h->np, (cuuint64_t)h->nsub, tokens};
+  cuuint64_t strides[3] = {row, row * h->np, row * h->np * h->nsub};
+  cuuint32_t box[4] = {box_cols, heads, 1, box_tokens};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q_pack), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_for(box_cols * 2), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The parts of a launch of the row attention that both callers share.
+struct RowsCall {
+  const __nv_bfloat16* q_pack;
+  int tokens, seqs;
+  const int* cu;
+  const int* lens;
+  const void* pool;          // bf16 pages
+  int num_pages;
+  const int* page_table;     // null: identity (see RowParams)
+  int pt_stride;
+  bool causal;
+  RowParams rp;              // results, status (the rest is filled in here)
+};
+
+cudaError_t launch_plan(const mlra_ctx* h, const RowsCall& c, int* status, cudaStream_t s) {
+  const int heads = h->heads_block < h->np ? h->heads_block : h->np;
+  RowPlanParams p = {};
+  p.cu = c.cu;
+  p.lens = c.lens;
+  p.batch = c.seqs;
+  p.total_q = c.tokens;
+  p.cap_len = c.pt_stride * kPage;
+  p.causal = c.causal;
+  p.plan = c.rp.plan;
+  p.status = status;
+  with_rows(h->var, [&](auto sh) {
+    using Sh = decltype(sh);
+    p.tile_tokens = Sh::NQ * (128 / heads);
+    p.key_tile = Sh::KT;
+    p.units = h->nsub * Sh::HALVES;
+    return 0;
+  });
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = launch_cfg(dim3(1), dim3(kPlanThreads), 0, s, true, &attr);
+  return cudaLaunchKernelEx(&cfg, mlra_rows_plan_kernel, p);
+}
+
+cudaError_t launch_rows(const mlra_ctx* h, const RowsCall& c, cudaStream_t s) {
+  return with_rows(h->var, [&](auto sh) {
+    using Sh = decltype(sh);
+    const uint64_t D = h->cfg.d_c + h->d_r;
+    RowParams p = c.rp;
+    p.page_table = c.page_table;
+    p.pt_stride = c.pt_stride;
+    p.num_pages = c.num_pages;
+    p.causal = c.causal;
+    p.nsub = h->nsub;
+    p.chunks = h->chunks;
+    p.heads_tile = h->heads_block < h->np ? h->heads_block : h->np;
+    p.tok_tile = 128 / p.heads_tile;
+    p.heads_block = h->heads_block;
+    p.vh = h->vh;
+    p.d_c = h->cfg.d_c;
+    CUtensorMap mc, mr, mqc, mqr;
+    if (!make_map(&mc, c.pool, (uint64_t)c.num_pages * kPage, D, D * 2, kPage, Sh::CW) ||
+        !make_map(&mr, c.pool, (uint64_t)c.num_pages * kPage, D, D * 2, kPage, Sh::RW) ||
+        !make_qpack_map(&mqc, h, c.q_pack, c.tokens, Sh::CW, p.heads_tile, p.tok_tile) ||
+        !make_qpack_map(&mqr, h, c.q_pack, c.tokens, Sh::RW, p.heads_tile, p.tok_tile))
+      return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = launch_cfg(dim3(h->num_sms), dim3(Sh::THREADS), Sh::SMEM, s, true, &attr);
+    return cudaLaunchKernelEx(&cfg, mlra_rows_kernel<Sh>, mc, mr, mqc, mqr, p);
+  });
+}
+
+cudaError_t launch_merge(const mlra_ctx* h, const RowsCall& c, cudaStream_t s) {
+  return with_rows(h->var, [&](auto sh) {
+    using Sh = decltype(sh);
+    MergeParams m = {};
+    m.plan = c.rp.plan;
+    m.ctas = h->num_sms;
+    m.causal = c.causal;
+    m.key_tile = Sh::KT;
+    m.halves = Sh::HALVES;
+    m.chunks = h->chunks;
+    m.heads_tile = h->heads_block < h->np ? h->heads_block : h->np;
+    m.tok_tile = 128 / m.heads_tile;
+    m.heads_block = h->heads_block;
+    m.vh = h->vh;
+    m.db = Sh::DB;
+    m.dv = Sh::DV;
+    m.rows = Sh::ROWS;
+    m.part_o = c.rp.part_o;
+    m.part_lse = c.rp.part_lse;
+    m.o_bf16 = c.rp.o_bf16;
+    m.lse = c.rp.lse;
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = launch_cfg(dim3(h->num_sms, 8), dim3(256), 0, s, true, &attr);
+    return cudaLaunchKernelEx(&cfg, mlra_rows_merge_kernel, m);
+  });
+}
+
+template <int DBB, int DH, int SUMK>
+cudaError_t launch_up(const mlra_ctx* h, const __nv_bfloat16* o, int tokens, const UpParams& up, cudaStream_t s) {
+  using Sh = UpShape<DBB, DH, SUMK>;
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return cudaErrorInvalidValue;
+  CUtensorMap mo;
+  cuuint64_t dims[3] = {(cuuint64_t)DBB, (cuuint64_t)h->vh, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)DBB * 2, (cuuint64_t)h->vh * DBB * 2};
+  cuuint32_t box[3] = {(cuuint32_t)Sh::CW, 1, 128};
+  cuuint32_t estr[3] = {1, 1, 1};
+  if (fn(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(o), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_for(Sh::CW * 2), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  // two CTAs an SM where shared memory holds them; no more CTAs than (head, token tile) items
+  const int per_sm = 2 * (Sh::SMEM + 1024) <= 227 * 1024 ? 2 : 1;
+  const long long items = (long long)up.heads * ((tokens + 127) / 128);
+  const int grid = (int)(items < (long long)h->num_sms * per_sm ? items : (long long)h->num_sms * per_sm);
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = launch_cfg(dim3(grid), dim3(Sh::THREADS), Sh::SMEM, s, true, &attr);
+  return cudaLaunchKernelEx(&cfg, mlra_rows_up_kernel<Sh>, h->map_wuv, mo, up);
+}
+
+// bf16 absorb for every variant (the E4M3 cache's scales go into the two query scales)
+cudaError_t dispatch_absorb_rows(const mlra_ctx* h, const ProjParams& pp, int tokens, cudaStream_t s) {
+  switch (h->var) {
+    case kTiny: return dispatch_absorb<32, 32>(h, pp, tokens, s);
+    case kMlra2: case kMlra2Sum: return dispatch_absorb<256, 128>(h, pp, tokens, s);
+    case kMla: return dispatch_absorb<512, 128>(h, pp, tokens, s);
+    default: return dispatch_absorb<128, 128>(h, pp, tokens, s);
+  }
+}
+
+ProjParams absorb_params(const mlra_ctx* h, const void* q, mlra_dtype q_dtype, int tokens, __nv_bfloat16* q_pack,
+                         int* status, const EarlyTags& tags) {
+  ProjParams pp = {};
+  pp.q = q;
+  pp.q_f32 = q_dtype == MLRA_F32;
+  pp.q_pack = q_pack;
+  pp.qscale = h->scale * kLog2e * (h->fp8 ? h->latent_scale : 1.f);
+  pp.qscale_rope = h->scale * kLog2e * (h->fp8 ? h->rope_scale : 1.f);
+  pp.d_r = h->d_r;
+  pp.np = h->np;
+  pp.nsub = h->nsub;
+  pp.chunks = h->chunks;
+  pp.heads_block = h->heads_block;
+  pp.batch = tokens;
+  pp.h = h->vh;
+  pp.q_heads = h->cfg.h;
+  pp.out_heads = h->cfg.h;
+  pp.out_scale = h->summed ? h->alpha : 1.f;
+  pp.q_rows_per_sub = h->np;
+  pp.status = status;
+  pp.tags = tags;
+  pp.wait_limit_ns = kWaitLimitNs;
+  return pp;
+}
+
+bool rows_sizes_ok(int total_q, int batch, int pt_stride) {
+  return total_q >= 0 && total_q <= kMaxQueryTokens && batch > 0 && batch <= kMaxSeqs && pt_stride > 0 &&
+         (long long)pt_stride * kPage <= 0x7fffffffLL - kTile;
+}
+
+int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t* cu, int total_q, const void* pool,
+                int num_pages, const int32_t* page_table, int pt_stride, const int32_t* seq_lens, int batch, void* out,
+                mlra_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  if (!h || !cu || !pool || !page_table || !seq_lens || !workspace || (total_q > 0 && (!q || !out)))
+    return MLRA_ERR_INVALID_ARG;
+  if (!rows_sizes_ok(total_q, batch, pt_stride) || num_pages <= 0) return MLRA_ERR_INVALID_ARG;
+  if ((q_dtype != MLRA_F32 && q_dtype != MLRA_BF16) || (out_dtype != MLRA_F32 && out_dtype != MLRA_BF16))
+    return MLRA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(pool) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return MLRA_ERR_INVALID_ARG;
+  if ((long long)num_pages * kPage > 0x7fffffffLL ||
+      (h->fp8 && (long long)batch * pt_stride * kPage > 0x7fffffffLL))
+    return MLRA_ERR_UNSUPPORTED;
+  PrefillWorkspace w = carve_prefill(h, total_q, batch, pt_stride, workspace);
+  if (ws_bytes < w.bytes) return MLRA_ERR_WORKSPACE;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != h->device) return MLRA_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (total_q == 0)
+    return cudaMemsetAsync(w.status, 0, 4, s) == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
+
+  const EarlyTags tags = {reinterpret_cast<unsigned*>(w.status) + 1, next_call_tag()};
+  const ProjParams pp = absorb_params(h, q, q_dtype, total_q, w.q_pack, w.status, tags);
+  RowsCall c = {};
+  c.q_pack = w.q_pack;
+  c.tokens = total_q;
+  c.seqs = batch;
+  c.cu = cu;
+  c.lens = seq_lens;
+  c.pool = h->fp8 ? static_cast<const void*>(w.pages) : pool;
+  c.num_pages = h->fp8 ? batch * pt_stride : num_pages;
+  c.page_table = h->fp8 ? nullptr : page_table;
+  c.pt_stride = pt_stride;
+  c.causal = true;
+  c.rp.plan = w.rows.plan;
+  c.rp.o_scale = h->fp8 ? h->latent_scale : 1.f;
+  c.rp.o_bf16 = w.o;
+  c.rp.lse = lse;
+  c.rp.part_o = w.rows.part_o;
+  c.rp.part_lse = w.rows.part_lse;
+  c.rp.status = w.status;
+  c.rp.tags = tags;
+  c.rp.wait_limit_ns = kWaitLimitNs;
+
+  g_use_pdl = true;
+  cudaError_t e = dispatch_absorb_rows(h, pp, total_q, s);
+  if (e == cudaSuccess && h->fp8) {
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = launch_cfg(dim3(pt_stride, batch), dim3(256), 0, s, true, &attr);
+    e = cudaLaunchKernelEx(&cfg, mlra_widen_pages_kernel, static_cast<const uint8_t*>(pool), num_pages, page_table,
+                           pt_stride, seq_lens, h->cfg.d_c + h->d_r, w.pages, w.status);
+  }
+  if (e == cudaSuccess) e = launch_plan(h, c, w.status, s);
+  if (e == cudaSuccess) e = launch_rows(h, c, s);
+  if (e == cudaSuccess) e = launch_merge(h, c, s);
+  if (e == cudaSuccess) {
+    const UpParams up = {w.rows.plan.hdr + 1, out, out_dtype == MLRA_F32, h->cfg.h, h->summed ? h->alpha : 1.f,
+                         w.status, kWaitLimitNs};
+    switch (h->var) {
+      case kTiny: e = h->summed ? launch_up<32, 32, 4>(h, w.o, total_q, up, s) : launch_up<32, 32, 1>(h, w.o, total_q, up, s); break;
+      case kMlra2: e = launch_up<256, 128, 1>(h, w.o, total_q, up, s); break;
+      case kMlra2Sum: e = launch_up<256, 128, 2>(h, w.o, total_q, up, s); break;
+      case kMla: e = launch_up<512, 128, 1>(h, w.o, total_q, up, s); break;
+      case kMlra4Sum: e = launch_up<128, 128, 4>(h, w.o, total_q, up, s); break;
+      default: e = launch_up<128, 128, 1>(h, w.o, total_q, up, s); break;
+    }
+  }
+  return e == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
+}
+
+int run_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const void* pool, int num_pages,
+                      const int32_t* prefix_table, int prefix_stride, const int32_t* prefix_lens,
+                      const int32_t* group_offsets, int groups, const int32_t* page_table, int pt_stride,
+                      const int32_t* seq_lens, int batch, void* out, mlra_dtype out_dtype, float* lse,
+                      void* workspace, size_t ws_bytes, void* stream) {
+  if (!h || !q || !pool || !prefix_table || !prefix_lens || !group_offsets || !page_table || !seq_lens || !out ||
+      !workspace)
+    return MLRA_ERR_INVALID_ARG;
+  if (h->fp8) return MLRA_ERR_UNSUPPORTED;
+  if (!rows_sizes_ok(batch, groups, prefix_stride) || batch <= 0 || batch > 4096 || num_pages <= 0 || pt_stride <= 0)
+    return MLRA_ERR_INVALID_ARG;
+  if ((q_dtype != MLRA_F32 && q_dtype != MLRA_BF16) || (out_dtype != MLRA_F32 && out_dtype != MLRA_BF16))
+    return MLRA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(pool) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return MLRA_ERR_INVALID_ARG;
+  if ((long long)num_pages * kPage > 0x7fffffffLL) return MLRA_ERR_UNSUPPORTED;
+  PrefixWorkspace w = carve_prefix(h, batch, groups, workspace);
+  if (ws_bytes < w.bytes) return MLRA_ERR_WORKSPACE;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != h->device) return MLRA_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  const EarlyTags tags = {reinterpret_cast<unsigned*>(w.dec.status) + 1, next_call_tag()};
+  ProjParams pp = absorb_params(h, q, q_dtype, batch, w.dec.q_pack, w.dec.status, tags);
+  pp.o_part = w.dec.o_part;
+  pp.lse_part = w.dec.lse_part;
+  pp.out = out;
+  pp.out_f32 = out_dtype == MLRA_F32;
+  pp.lse_out = lse;
+  pp.seq_lens = seq_lens;
+  pp.pt_stride = pt_stride;
+  pp.groups = h->groups;
+
+  RowsCall c = {};
+  c.q_pack = w.dec.q_pack;
+  c.tokens = batch;
+  c.seqs = groups;
+  c.cu = group_offsets;
+  c.lens = prefix_lens;
+  c.pool = pool;
+  c.num_pages = num_pages;
+  c.page_table = prefix_table;
+  c.pt_stride = prefix_stride;
+  c.causal = false;
+  c.rp.plan = w.rows.plan;
+  c.rp.o_scale = 1.f;
+  c.rp.o_f32 = w.o;
+  c.rp.lse = w.lse;
+  c.rp.part_o = w.rows.part_o;
+  c.rp.part_lse = w.rows.part_lse;
+  c.rp.status = w.dec.status;
+  c.rp.tags = tags;
+  c.rp.wait_limit_ns = kWaitLimitNs;
+
+  DecodeParams dp = {};
+  dp.seq_lens = seq_lens;
+  dp.page_table = page_table;
+  dp.pt_stride = pt_stride;
+  dp.batch = batch;
+  dp.num_pages = num_pages;
+  dp.groups = h->groups;
+  dp.nsub = h->nsub;
+  dp.chunks = h->chunks;
+  dp.heads_block = h->heads_block;
+  dp.h = h->vh;
+  dp.d_c = h->cfg.d_c;
+  dp.q_rows = h->heads_block < h->np ? h->heads_block : h->np;
+  dp.o_scale = 1.f;
+  dp.o_part = w.dec.o_part;
+  dp.lse_part = w.dec.lse_part;
+  dp.status = w.dec.status;
+  dp.tags = tags;
+  dp.wait_limit_ns = kWaitLimitNs;
+
+  PrefixParts& pre = pp.prefix;
+  pre.plan = w.rows.plan;
+  pre.ctas = h->num_sms;
+  pre.chunks = h->chunks;
+  pre.heads_tile = dp.q_rows;
+  pre.tok_tile = 128 / dp.q_rows;
+  pre.o_dense = w.o;
+  pre.lse_dense = w.lse;
+  pre.part_o = w.rows.part_o;
+  pre.part_lse = w.rows.part_lse;
+  with_rows(h->var, [&](auto sh) {
+    using Sh = decltype(sh);
+    pre.units = h->nsub * Sh::HALVES;
+    pre.halves = Sh::HALVES;
+    pre.key_tile = Sh::KT;
+    pre.rows = Sh::ROWS;
+    pre.dv = Sh::DV;
+    return 0;
+  });
+
+  const int D = h->cfg.d_c + h->d_r;
+  const int cw = h->d_b < 64 ? h->d_b : 64, rw = h->d_r < 64 ? h->d_r : 64;
+  CUtensorMap mc, mr, mqc, mqr;
+  const uint64_t qrows = (uint64_t)batch * h->nsub * h->np, qw = h->d_b + h->d_r;
+  if (!make_map(&mc, pool, (uint64_t)num_pages * kPage, D, (uint64_t)D * 2, kPage, cw) ||
+      !make_map(&mr, pool, (uint64_t)num_pages * kPage, D, (uint64_t)D * 2, kPage, rw) ||
+      !make_map(&mqc, w.dec.q_pack, qrows, qw, qw * 2, dp.q_rows, cw) ||
+      !make_map(&mqr, w.dec.q_pack, qrows, qw, qw * 2, dp.q_rows, rw))
+    return MLRA_ERR_CUDA;
+
+  g_use_pdl = true;
+  cudaError_t e = dispatch_absorb_rows(h, pp, batch, s);
+  if (e == cudaSuccess) e = launch_plan(h, c, w.dec.status, s);
+  if (e == cudaSuccess) switch (h->var) {
+      case kTiny: e = launch_decode<DecTiny>(h, mc, mr, mqc, mqr, dp, s); break;
+      case kMlra4: e = launch_decode<DecMlra4>(h, mc, mr, mqc, mqr, dp, s); break;
+      case kMlra4Sum: e = launch_decode<DecMlra4Sum>(h, mc, mr, mqc, mqr, dp, s); break;
+      case kMla: e = launch_decode<DecMla>(h, mc, mr, mqc, mqr, dp, s); break;
+      default: e = launch_decode<DecMlra2>(h, mc, mr, mqc, mqr, dp, s); break;
+    }
+  if (e == cudaSuccess) e = launch_rows(h, c, s);
+  if (e == cudaSuccess) switch (h->var) {
+      case kTiny:
+        e = h->summed ? dispatch_uproj_prefix<128, 32, 4>(h, pp, batch, s) : dispatch_uproj_prefix<32, 32, 1>(h, pp, batch, s);
+        break;
+      case kMlra4: e = dispatch_uproj_prefix<128, 128, 1>(h, pp, batch, s); break;
+      case kMlra4Sum: e = dispatch_uproj_prefix<512, 128, 4>(h, pp, batch, s); break;
+      case kMlra2: e = dispatch_uproj_prefix<256, 128, 1>(h, pp, batch, s); break;
+      case kMlra2Sum: e = dispatch_uproj_prefix<512, 128, 2>(h, pp, batch, s); break;
+      default: e = dispatch_uproj_prefix<512, 128, 1>(h, pp, batch, s); break;
+    }
+  return e == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
+}
+
+}  // namespace

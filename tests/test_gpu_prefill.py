@@ -1,0 +1,272 @@
+"""Prompt attention (mlra_prefill) on the GPU against the float64 oracle, token by token.
+
+The oracle side is ``O.decode_sequence`` / ``O.decode_heads`` on the prefix of cached rows each
+token may see. Tolerances: outputs of ordinary inputs (N(0,1) cache and queries) use the decode
+path's parity bar (tests/gpu_util.py); the chain rounds the same quantities to bf16 (absorbed
+query, probabilities, latent result, each off by at most 2^-8 / 2 relative), so the same bar holds.
+"""
+import numpy as np
+import pytest
+import torch
+
+import rank_latent_kv_mlra_b200 as M
+import workloads as W
+from oracle import mlra_oracle as O
+from tests import gpu_util as G
+
+pytestmark = pytest.mark.gpu
+
+MLRA4 = W.WORKLOADS["mlra4_h128_b32_n8192"]
+MLRA2 = W.WORKLOADS["mlra2_h128_b64_n4096"]
+MLA = W.WORKLOADS["mla_h128_b128_ragged1k_32k"]
+TINY = W.scaled(W.WORKLOADS["mlra4_h8_b1_n256_f32"], paging="permuted")
+RANK4 = W.WORKLOADS["tp4rank_mlra4_h32_b64_n8192"]
+E4M3 = W.WORKLOADS["mlra4fp8_h128_b32_n8192"]
+SUM4 = W.WORKLOADS["mlra4sum_h128_b32_n8192"]
+SUM2 = W.WORKLOADS["mlra2sum_h128_b64_n4096"]
+TINYSUM = W.scaled(TINY, summed=True)
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    M.load_library()
+
+
+def make(w, n_q, past, seed=0, q_dtype=torch.bfloat16, behind=0):
+    """Packed queries for `n_q[b]` new tokens of sequences with `past[b]` older ones."""
+    total = [a + b for a, b in zip(n_q, past)]
+    w = W.scaled(w, batch=len(n_q), seq_len=None, len_range=(1, 1), seed=seed + 100)
+    inp = W.make_workload(w, device="cuda", seq_lens=torch.tensor(total, dtype=torch.int32), extra_pages=2)
+    cu = np.concatenate([[0], np.cumsum(n_q)]).astype(np.int32)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    q = torch.randn(int(cu[-1]) + behind, w.h, w.d_h + w.d_r, generator=g, device="cuda")
+    inp["q"] = q.to(q_dtype)
+    inp["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    return w, inp
+
+
+def handle(w, inp):
+    fp8 = dict(cache_fp8=True, latent_scale=W.E4M3_SCALE, rope_scale=W.E4M3_SCALE) if w.cache == "e4m3" else {}
+    return M.mlra_create(w.h, w.d_h, w.d_c, w.d_r, w.k, inp["w_uk"], inp["w_uv"], blocks_summed=w.summed, **fp8)
+
+
+def run(hdl, w, inp, out_dtype=torch.float32, workspace=None, stream=None):
+    total = inp["q"].shape[0]
+    out = torch.full((total, w.h, w.d_h), float("nan"), device="cuda", dtype=out_dtype)
+    lse = torch.full((total, w.h * (w.k if w.summed else 1)), float("nan"), device="cuda")
+    ws = M.mlra_prefill(hdl, inp["q"], inp["cu"], inp["pool"], inp["page_table"], inp["seq_lens"], out, lse,
+                        workspace=workspace, stream=stream)
+    torch.cuda.synchronize()
+    return out, lse, M.mlra_get_status(ws)
+
+
+def rows64(w, inp, b):
+    rows = W.logical_rows(inp, b)
+    if w.cache == "e4m3":
+        return rows.view(torch.float8_e4m3fn).double() * W.E4M3_SCALE
+    return rows.double()
+
+
+def reference(w, inp):
+    """float64 outputs and lse of every packed token (torch on the GPU, from the definition: each
+    head's keys and values formed from its block of the cached rows)."""
+    cu = inp["cu"].tolist()
+    q = inp["q"].to(torch.bfloat16).double()
+    wuk, wuv = inp["w_uk"].double(), inp["w_uv"].double()
+    total = cu[-1]
+    blocks = w.k if w.summed else 1
+    out = torch.zeros(total, w.h, w.d_h, dtype=torch.float64, device="cuda")
+    lse = torch.full((total, blocks, w.h), -np.inf, dtype=torch.float64, device="cuda")
+    scale = 1.0 / np.sqrt(w.d_h + w.d_r)
+    hb = w.h // w.k
+    for b in range(len(cu) - 1):
+        n, T = cu[b + 1] - cu[b], int(inp["seq_lens"][b])
+        if n == 0 or T == 0:
+            continue
+        rows = rows64(w, inp, b)
+        pos = torch.arange(T - n, T, device="cuda")
+        mask = torch.arange(T, device="cuda")[None, :] > pos[:, None]
+        for h in range(w.h):
+            for j in range(blocks):
+                blk = j if w.summed else h // hb
+                uk, uv = (wuk[j, h], wuv[j, h]) if w.summed else (wuk[h], wuv[h])
+                c = rows[:, blk * w.d_b:(blk + 1) * w.d_b]
+                key = torch.cat([c @ uk, rows[:, w.d_c:]], dim=1)
+                s = (q[cu[b]:cu[b + 1], h] @ key.t() * scale).masked_fill(mask, -np.inf)
+                l = torch.logsumexp(s, dim=1)
+                p = torch.where(mask, 0.0, torch.exp(s - torch.where(l.isinf(), 0.0, l)[:, None]))
+                alpha = 1.0 / np.sqrt(w.k) if w.summed else 1.0
+                out[cu[b]:cu[b + 1], h] += alpha * (p @ (c @ uv))
+                lse[cu[b]:cu[b + 1], j, h] = l
+    return out.cpu().numpy(), lse.reshape(total, -1).cpu().numpy()
+
+
+def check(w, inp, out, lse, status, what, rows=1.0):
+    """`rows`: factor of the cached rows against N(0,1). The bar's absolute parts are for N(0,1)
+    rows. The rounding of the absorbed query moves a score by an amount that grows with the row
+    (x rows), a probability moves by its score's error relative to itself, and the values it
+    weighs are x rows too: absolute output errors grow by rows^2, those of the lse by rows. The
+    relative part of the bar stays."""
+    assert status == 0, M.mlra_status_string(status)
+    ref, rlse = reference(w, inp)
+    total = ref.shape[0]
+    G.assert_parity(out[:total].float().cpu().numpy(), ref, what, tol_max=G.TOL_MAX_ABS * rows ** 2,
+                    tol_mean=G.TOL_MEAN_ABS * rows ** 2)
+    got = lse[:total].cpu().numpy()
+    live = np.isfinite(rlse)
+    assert np.array_equal(np.isneginf(got), ~live), what
+    assert np.abs(got[live] - rlse[live]).max(initial=0.0) < G.TOL_LSE_ABS * rows, what
+
+
+CASES = {
+    # name: (workload, new tokens, older tokens)
+    "one_token": (MLRA4, [1], [0]),
+    "one_token_long": (MLRA4, [1], [1000]),
+    "tile_edges": (MLRA4, [3, 4, 5, 8, 9, 127, 128, 129], [0, 64, 63, 0, 65, 1, 0, 127]),
+    "empty_sequences": (MLRA4, [0, 7, 0, 0, 130, 0], [0, 0, 300, 0, 5, 64]),
+    "ragged": (MLRA4, [333, 1, 64, 511, 20], [0, 0, 0, 77, 700]),
+    "long_chunk": (MLRA4, [200], [3000]),
+    "mlra2": (MLRA2, [1, 2, 3, 150, 65], [0, 63, 500, 0, 130]),
+    "mla": (MLA, [1, 2, 70, 33], [0, 63, 10, 400]),
+    "rank4": (RANK4, [5, 130, 1, 64], [0, 40, 200, 0]),
+    "tiny": (TINY, [1, 63, 64, 65, 200, 0, 300], [0, 1, 0, 100, 0, 9, 57]),
+    "e4m3": (E4M3, [5, 130, 1, 64], [0, 40, 200, 700]),
+    "sum4": (SUM4, [5, 70, 1], [0, 40, 300]),
+    "sum2": (SUM2, [5, 70, 1], [0, 40, 300]),
+    "tinysum": (TINYSUM, [5, 70, 1, 130], [0, 40, 300, 0]),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_matches_the_definition(name):
+    w, n, past = CASES[name]
+    w, inp = make(w, n, past, seed=len(name))
+    hdl = handle(w, inp)
+    for dt in (torch.float32, torch.bfloat16):
+        check(w, inp, *run(hdl, w, inp, dt), f"{name} {dt}")
+
+
+def test_fp32_query():
+    w, inp = make(MLRA4, [40, 3], [0, 90], seed=5, q_dtype=torch.float32)
+    check(w, inp, *run(handle(w, inp), w, inp), "fp32 query")
+
+
+def test_tokens_without_keys():
+    """Sequences shorter than their query tokens: positions below 0 see nothing."""
+    w, inp = make(MLRA4, [20, 6, 9], [0, 0, 3], seed=6)
+    inp["seq_lens"] = torch.tensor([13, 0, 12], dtype=torch.int32, device="cuda")
+    out, lse, status = run(handle(w, inp), w, inp)
+    check(w, inp, out, lse, status, "short sequences")
+    assert (out[:7] == 0).all() and (out[20:26] == 0).all()
+
+
+def test_rows_behind_the_last_sequence_stay():
+    w, inp = make(MLRA4, [30, 41], [0, 7], seed=7, behind=60)
+    out, lse, status = run(handle(w, inp), w, inp)
+    check(w, inp, out, lse, status, "padded batch")
+    assert out[71:].isnan().all() and lse[71:].isnan().all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_bad_cached_row_reaches_only_the_tokens_that_see_it(value):
+    """Token 100's row holds NaN (or infinities): tokens before it keep the results they had."""
+    w, inp = make(MLRA4, [160], [0], seed=8)
+    hdl = handle(w, inp)
+    clean, clean_lse, _ = run(hdl, w, inp)
+    page = int(inp["page_table"][0, 100 // 64])
+    inp["pool"][page, 100 % 64] = value
+    out, lse, status = run(hdl, w, inp)
+    assert status == 0
+    assert torch.equal(out[:100], clean[:100]) and torch.equal(lse[:100], clean_lse[:100])
+    assert out[100:].isnan().all()
+
+
+def test_runs_are_bit_identical_and_the_split_is_exact():
+    """Two runs give the same bits, and a chunked prompt gives the whole prompt's results to
+    within the rounding of P and of the merged parts."""
+    w, inp = make(MLRA4, [700], [0], seed=9)
+    hdl = handle(w, inp)
+    a, la, _ = run(hdl, w, inp)
+    b, lb, _ = run(hdl, w, inp)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    pieces = []
+    for lo, hi in ((0, 1), (1, 300), (300, 555), (555, 700)):
+        part = dict(inp, q=inp["q"][lo:hi].contiguous(), cu=torch.tensor([0, hi - lo], dtype=torch.int32, device="cuda"),
+                    seq_lens=torch.tensor([hi], dtype=torch.int32, device="cuda"))
+        pieces.append(run(hdl, w, part)[0])
+    G.assert_parity(torch.cat(pieces).cpu().numpy(), a.double().cpu().numpy(), "chunks")
+
+
+def test_prefill_then_decode_agree_on_the_last_token():
+    w, inp = make(MLRA4, [1, 1, 1], [200, 63, 511], seed=10)
+    hdl = handle(w, inp)
+    out, lse, _ = run(hdl, w, inp)
+    dout = torch.empty_like(out)
+    dlse = torch.empty_like(lse)
+    M.mlra_decode(hdl, inp["q"], inp["pool"], inp["page_table"], inp["seq_lens"], dout, dlse)
+    torch.cuda.synchronize()
+    G.assert_parity(out.cpu().numpy(), dout.double().cpu().numpy(), "prefill against decode")
+    assert (lse - dlse).abs().max() < 1e-3
+
+
+def test_large_scores_raise_the_running_maximum():
+    """Keys whose scores grow along the sequence make the kernel raise its maximum and rescale."""
+    w, inp = make(MLRA4, [260], [700], seed=11)
+    ramp = torch.linspace(0.1, 6.0, 960, device="cuda")
+    for t in range(960):
+        page = int(inp["page_table"][0, t // 64])
+        inp["pool"][page, t % 64] *= ramp[t]
+    check(w, inp, *run(handle(w, inp), w, inp), "ramp", rows=6.0)
+
+
+def test_captured_graph_replays_with_new_inputs():
+    w, inp = make(MLRA4, [33, 90], [10, 0], seed=12)
+    hdl = handle(w, inp)
+    out = torch.empty(123, w.h, w.d_h, device="cuda")
+    ws = torch.empty(M.mlra_prefill_workspace_size(hdl, 123, 2, inp["page_table"].shape[1]), dtype=torch.uint8,
+                     device="cuda")
+    args = (inp["q"], inp["cu"], inp["pool"], inp["page_table"], inp["seq_lens"], out)
+    M.mlra_prefill(hdl, *args, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.mlra_prefill(hdl, *args, workspace=ws)
+    inp["q"].copy_(torch.randn_like(inp["q"]))
+    inp["cu"].copy_(torch.tensor([0, 50, 123], dtype=torch.int32))
+    inp["seq_lens"].copy_(torch.tensor([43, 80], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    got = out.clone()
+    ref, _, status = run(hdl, w, inp)
+    assert status == 0 and torch.equal(got, ref)
+
+
+def test_another_stream():
+    w, inp = make(MLRA4, [33, 90], [10, 0], seed=13)
+    hdl = handle(w, inp)
+    ref, _, _ = run(hdl, w, inp)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, _, status = run(hdl, w, inp, stream=s)
+    assert status == 0 and torch.equal(out, ref)
+
+
+def test_status_of_bad_lengths_and_pages():
+    """Bad device-side inputs that the kernels' own checks turn into a status."""
+    w, inp = make(MLRA4, [33, 90], [10, 0], seed=14)
+    hdl = handle(w, inp)
+    good = run(hdl, w, inp)[0]
+    bad = dict(inp, seq_lens=torch.tensor([43, 10 ** 6], dtype=torch.int32, device="cuda"))
+    assert run(hdl, w, bad)[2] == -7
+    for cu in ([0, 40, 33], [1, 33, 123], [0, 33, 400], [0, -5, 123]):
+        bad = dict(inp, cu=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        out, _, status = run(hdl, w, bad)
+        assert status == -7 and out.isnan().all()
+    pt = inp["page_table"].clone()
+    pt[0, 0] = inp["pool"].shape[0]
+    out, _, status = run(hdl, w, dict(inp, page_table=pt))
+    assert status == -4
+    assert torch.equal(run(hdl, w, inp)[0], good)
