@@ -51,6 +51,7 @@ typedef enum {
   MLRA_ERR_WORKSPACE = -6,     /* workspace smaller than mlra_workspace_size */
   MLRA_ERR_SEQ_LEN = -7,       /* device: seq_len < 0 or > pt_stride * page_size */
   MLRA_ERR_SCRATCH_LIMIT = -8, /* mlra_decode_noalloc: batch too large for its fixed scratch */
+  MLRA_ERR_NO_PAGES = -10,     /* device: fewer free pages than a page operator needs */
   MLRA_ERR_DRAIN = -9          /* device: after a wait timed out, copies or MMAs still in flight
                                   did not finish within the limit either, so shared memory or
                                   tensor memory may have been released under them. The CUDA
@@ -289,6 +290,52 @@ int mlra_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const v
                        const int32_t* group_offsets, int groups, const int32_t* page_table, int pt_stride,
                        const int32_t* seq_lens, int batch, void* out, mlra_dtype out_dtype, float* lse,
                        void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- The pages of the cache ----
+ * State, all of it the caller's device memory: page_table int32 [batch][pt_stride] and seq_lens
+ * int32 [batch] as in mlra_decode, and refs int32 [num_pages], the number of page-table entries
+ * that hold each page (0: the page is free). Row b holds the first ceil(seq_lens[b] / page_size)
+ * entries; entries behind them mean nothing and are left as they are. A row with seq_lens 0 is
+ * empty. Full pages may be held by several rows; a partly filled last page by one.
+ * New pages are the lowest-numbered free ones, in the order of the requests, then of the pages
+ * within a request: results do not depend on timing. A reserved page's slots keep what they held.
+ * Each operator clears and sets the status word (the first 4 bytes of `workspace`) and either does
+ * all of its work or, where it reports MLRA_ERR_SEQ_LEN or MLRA_ERR_NO_PAGES for its requests,
+ * changes nothing. A page-table entry outside [0, num_pages) is passed over and reported as
+ * MLRA_ERR_PAGE_OOB. Requests (n <= batch of them) are device int32 arrays. n = 0 is allowed.
+ * batch <= 65536, num_pages <= 2^25. Calls on one state must follow one another in stream order.
+ * Launches two kernels each (compaction three), chained by programmatic dependent launch. */
+
+/* Bytes of device workspace the page operators need (host output). */
+int mlra_pages_workspace_size(mlra_handle h, int num_pages, int batch, size_t* bytes);
+
+/* Gives row seq_ids[i] the pages for new_lens[i] cached rows and sets seq_lens to that: a new
+ * sequence in an empty row, or room for a running one's next tokens (write them with
+ * mlra_append_cache or mlra_project_append). MLRA_ERR_SEQ_LEN: a row named twice or outside
+ * [0, batch), or a new length below the present one or above pt_stride * page_size. */
+int mlra_reserve_pages(mlra_handle h, int32_t* refs, int num_pages, int32_t* page_table, int pt_stride, int batch,
+                       int32_t* seq_lens, const int32_t* seq_ids, const int32_t* new_lens, int n, void* workspace,
+                       size_t ws_bytes, void* stream);
+
+/* Makes row dst_ids[i] a copy of sequence src_ids[i]: full pages are shared, the rows of a partly
+ * filled last page are copied to a new page (slots behind them keep what they held), so both go on
+ * on their own. Several forks may have one source. MLRA_ERR_SEQ_LEN: a destination named twice, not
+ * empty, or also a source; a row outside [0, batch). */
+int mlra_fork_pages(mlra_handle h, void* pool, int32_t* refs, int num_pages, int32_t* page_table, int pt_stride,
+                    int batch, int32_t* seq_lens, const int32_t* src_ids, const int32_t* dst_ids, int n,
+                    void* workspace, size_t ws_bytes, void* stream);
+
+/* Empties row seq_ids[i]: its entries give up their pages and seq_lens becomes 0. Freeing an empty
+ * row is allowed. MLRA_ERR_SEQ_LEN: a row named twice or outside [0, batch). */
+int mlra_free_pages(mlra_handle h, int32_t* refs, int num_pages, int32_t* page_table, int pt_stride, int batch,
+                    int32_t* seq_lens, const int32_t* seq_ids, int n, void* workspace, size_t ws_bytes, void* stream);
+
+/* Moves the used pages to the front: with U pages in use, the i-th used page numbered U or above
+ * moves to the i-th free one below U (contents, count, and every row's entries), after which pages
+ * U .. num_pages - 1 are free. `used` (device int32, or NULL) receives U. Every entry that refs
+ * counts must be in page_table. */
+int mlra_compact_pages(mlra_handle h, void* pool, int32_t* refs, int num_pages, int32_t* page_table, int pt_stride,
+                       int batch, int32_t* seq_lens, int32_t* used, void* workspace, size_t ws_bytes, void* stream);
 
 /* Runs the device split planner on seq_lens and writes the segments it would process:
  * segments device int32 [max_segments][5] rows (b, group, tile_begin, tile_end, slot),

@@ -31,6 +31,7 @@ STATUS = {
     -7: "MLRA_ERR_SEQ_LEN",
     -8: "MLRA_ERR_SCRATCH_LIMIT",
     -9: "MLRA_ERR_DRAIN",
+    -10: "MLRA_ERR_NO_PAGES",
 }
 
 EXPORTED = [
@@ -38,6 +39,7 @@ EXPORTED = [
     "mlra_append_cache", "mlra_plan", "mlra_get_info", "mlra_get_status", "mlra_status_string",
     "mlra_decode_profiled", "mlra_decode_noalloc", "mlra_project_workspace_size", "mlra_project_append",
     "mlra_prefill_workspace_size", "mlra_prefill", "mlra_decode_prefix_workspace_size", "mlra_decode_prefix",
+    "mlra_pages_workspace_size", "mlra_reserve_pages", "mlra_fork_pages", "mlra_free_pages", "mlra_compact_pages",
 ]
 
 
@@ -89,6 +91,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mlra_prefill.argtypes = [P, P, I, P, I, P, I, P, I, P, I, P, I, P, P, S, P]
     lib.mlra_decode_prefix_workspace_size.argtypes = [P, I, I, ctypes.POINTER(S)]
     lib.mlra_decode_prefix.argtypes = [P, P, I, P, I, P, I, P, P, I, P, I, P, I, P, I, P, P, S, P]
+    lib.mlra_pages_workspace_size.argtypes = [P, I, I, ctypes.POINTER(S)]
+    lib.mlra_reserve_pages.argtypes = [P, P, I, P, I, I, P, P, P, I, P, S, P]
+    lib.mlra_fork_pages.argtypes = [P, P, P, I, P, I, I, P, P, P, I, P, S, P]
+    lib.mlra_free_pages.argtypes = [P, P, I, P, I, I, P, P, I, P, S, P]
+    lib.mlra_compact_pages.argtypes = [P, P, P, I, P, I, I, P, P, P, S, P]
     lib.mlra_plan.argtypes = [P, P, I, I, P, I, P, P]
     lib.mlra_get_info.argtypes = [P, ctypes.POINTER(mlra_info)]
     lib.mlra_get_status.argtypes = [P, ctypes.POINTER(I)]
@@ -442,6 +449,72 @@ def mlra_decode_prefix(handle: Handle, q, pool, prefix_table, prefix_lens, group
             _ptr(out), _dtype(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
             _stream(stream)), "mlra_decode_prefix")
     return workspace
+
+
+def mlra_pages_workspace_size(handle: Handle, num_pages: int, batch: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().mlra_pages_workspace_size(handle.ptr, num_pages, batch, ctypes.byref(n)),
+           "mlra_pages_workspace_size")
+    return n.value
+
+
+def _pages_call(name, handle, pool, refs, page_table, seq_lens, requests, workspace, stream, used=None):
+    """One page operator: checks, workspace, call. `pool` None and `requests` () where it has none."""
+    _require(refs, "refs", torch.int32)
+    _tables(page_table, seq_lens, ("page_table", "seq_lens"))
+    if refs.dim() != 1:
+        raise ValueError("refs must be [num_pages]")
+    named = dict(refs=refs, page_table=page_table, seq_lens=seq_lens, workspace=workspace, pool=pool, used=used)
+    if pool is not None:
+        _require(pool, "pool", _pool_dtype(handle))
+        cfg = handle.cfg
+        if tuple(pool.shape) != (refs.shape[0], cfg.page_size, cfg.d_c + cfg.d_rope):
+            raise ValueError("pool must be [num_pages][page_size][d_c + d_rope]")
+    if used is not None:
+        _require(used, "used", torch.int32)
+    for key, t in requests:
+        _require(t, key, torch.int32)
+        if t.dim() != 1 or t.shape != requests[0][1].shape:
+            raise ValueError("requests must be vectors of one length")
+        named[key] = t
+    dev = _on_one_device(**named)
+    B, n = page_table.shape[0], requests[0][1].shape[0] if requests else 0
+    with torch.cuda.device(dev):
+        workspace = _workspace(workspace, 0 if workspace is not None else
+                               mlra_pages_workspace_size(handle, refs.shape[0], B), dev, stream)
+        args = [handle.ptr] + ([] if pool is None else [_ptr(pool)])
+        args += [_ptr(refs), refs.shape[0], _ptr(page_table), page_table.shape[1], B, _ptr(seq_lens)]
+        args += [_ptr(t) for _, t in requests] + ([n] if requests else [_ptr(used)])
+        args += [_ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)]
+        _check(getattr(load_library(), name)(*args), name)
+    return workspace
+
+
+def mlra_reserve_pages(handle: Handle, refs, page_table, seq_lens, seq_ids, new_lens, workspace=None, stream=None):
+    """Gives each row of seq_ids the pages for new_lens cached rows (lowest-numbered free pages, in
+    order) and sets seq_lens to that. refs int32 [num_pages] counts the table entries that hold
+    each page. Returns the workspace, whose first int32 is the call's status word."""
+    return _pages_call("mlra_reserve_pages", handle, None, refs, page_table, seq_lens,
+                       [("seq_ids", seq_ids), ("new_lens", new_lens)], workspace, stream)
+
+
+def mlra_fork_pages(handle: Handle, pool, refs, page_table, seq_lens, src_ids, dst_ids, workspace=None, stream=None):
+    """Makes each row of dst_ids (empty rows) a copy of the sequence in src_ids: full pages shared,
+    the rows of a partly filled last page copied to a new page. Returns the workspace."""
+    return _pages_call("mlra_fork_pages", handle, pool, refs, page_table, seq_lens,
+                       [("src_ids", src_ids), ("dst_ids", dst_ids)], workspace, stream)
+
+
+def mlra_free_pages(handle: Handle, refs, page_table, seq_lens, seq_ids, workspace=None, stream=None):
+    """Empties the rows of seq_ids; pages that no row holds any more are free. Returns the workspace."""
+    return _pages_call("mlra_free_pages", handle, None, refs, page_table, seq_lens, [("seq_ids", seq_ids)], workspace,
+                       stream)
+
+
+def mlra_compact_pages(handle: Handle, pool, refs, page_table, seq_lens, used=None, workspace=None, stream=None):
+    """Moves the used pages to the front of the pool and renames them in every row. `used` (int32,
+    one element) receives their number. Returns the workspace."""
+    return _pages_call("mlra_compact_pages", handle, pool, refs, page_table, seq_lens, [], workspace, stream, used)
 
 
 def mlra_plan(handle: Handle, seq_lens, pt_stride: int, max_segments: int = 4096, stream=None):

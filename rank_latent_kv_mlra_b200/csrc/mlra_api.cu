@@ -19,6 +19,7 @@
 #include "common.cuh"
 #include "producer.cuh"
 #include "decode.cuh"
+#include "pages.cuh"
 #include "proj.cuh"
 #include "rows.cuh"
 
@@ -576,6 +577,7 @@ cudaError_t launch_down_proj(const CUtensorMap& mw, const CUtensorMap& mx, const
 }  // namespace
 
 #include "rows_api.cuh"
+#include "pages_api.cuh"
 
 extern "C" {
 
@@ -778,6 +780,74 @@ int mlra_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const v
                            stream);
 }
 
+int mlra_pages_workspace_size(mlra_handle h, int num_pages, int batch, size_t* bytes) {
+  if (!h || !bytes || !pages_sizes_ok(num_pages, batch, 1)) return MLRA_ERR_INVALID_ARG;
+  *bytes = carve_pages(num_pages, batch, nullptr).bytes;
+  return MLRA_OK;
+}
+
+int mlra_reserve_pages(mlra_handle h, int32_t* refs, int num_pages, int32_t* page_table, int pt_stride, int batch,
+                       int32_t* seq_lens, const int32_t* seq_ids, const int32_t* new_lens, int n, void* workspace,
+                       size_t ws_bytes, void* stream) {
+  PagesParams p;
+  const int rc = pages_params(h, nullptr, false, refs, num_pages, page_table, pt_stride, batch, seq_lens, seq_ids,
+                              new_lens, n, true, workspace, ws_bytes, &p);
+  if (rc != MLRA_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (n == 0) return pages_nothing(p, s);
+  g_use_pdl = true;
+  const int supers = (num_pages + kSuperPages - 1) / kSuperPages;
+  cudaError_t e = launch_pages(mlra_pages_scan_kernel<true, PageOp::kReserve>, dim3(supers + 1), p, s);
+  if (e == cudaSuccess) e = launch_pages(mlra_pages_reserve_kernel, dim3(n, 4), p, s);
+  return e == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
+}
+
+int mlra_fork_pages(mlra_handle h, void* pool, int32_t* refs, int num_pages, int32_t* page_table, int pt_stride,
+                    int batch, int32_t* seq_lens, const int32_t* src_ids, const int32_t* dst_ids, int n,
+                    void* workspace, size_t ws_bytes, void* stream) {
+  PagesParams p;
+  const int rc = pages_params(h, pool, true, refs, num_pages, page_table, pt_stride, batch, seq_lens, src_ids, dst_ids,
+                              n, true, workspace, ws_bytes, &p);
+  if (rc != MLRA_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (n == 0) return pages_nothing(p, s);
+  g_use_pdl = true;
+  const int supers = (num_pages + kSuperPages - 1) / kSuperPages;
+  cudaError_t e = launch_pages(mlra_pages_scan_kernel<true, PageOp::kFork>, dim3(supers + 1), p, s);
+  if (e == cudaSuccess) e = launch_pages(mlra_pages_fork_kernel, dim3(n, 4), p, s);
+  return e == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
+}
+
+int mlra_free_pages(mlra_handle h, int32_t* refs, int num_pages, int32_t* page_table, int pt_stride, int batch,
+                    int32_t* seq_lens, const int32_t* seq_ids, int n, void* workspace, size_t ws_bytes, void* stream) {
+  PagesParams p;
+  const int rc = pages_params(h, nullptr, false, refs, num_pages, page_table, pt_stride, batch, seq_lens, seq_ids,
+                              nullptr, n, false, workspace, ws_bytes, &p);
+  if (rc != MLRA_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (n == 0) return pages_nothing(p, s);
+  g_use_pdl = true;
+  cudaError_t e = launch_pages(mlra_pages_scan_kernel<true, PageOp::kFree>, dim3(1), p, s);
+  if (e == cudaSuccess) e = launch_pages(mlra_pages_free_kernel, dim3(n), p, s);
+  return e == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
+}
+
+int mlra_compact_pages(mlra_handle h, void* pool, int32_t* refs, int num_pages, int32_t* page_table, int pt_stride,
+                       int batch, int32_t* seq_lens, int32_t* used, void* workspace, size_t ws_bytes, void* stream) {
+  PagesParams p;
+  const int rc = pages_params(h, pool, true, refs, num_pages, page_table, pt_stride, batch, seq_lens, nullptr, nullptr,
+                              0, false, workspace, ws_bytes, &p);
+  if (rc != MLRA_OK) return rc;
+  p.used = used;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  g_use_pdl = true;
+  const int supers = (num_pages + kSuperPages - 1) / kSuperPages;
+  cudaError_t e = launch_pages(mlra_pages_scan_kernel<false, PageOp::kFree>, dim3(supers), p, s);
+  if (e == cudaSuccess) e = launch_pages(mlra_pages_move_kernel, dim3(h->num_sms * 6), p, s);
+  if (e == cudaSuccess) e = launch_pages(mlra_pages_remap_kernel, dim3(batch < 1024 ? batch : 1024), p, s);
+  return e == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
+}
+
 int mlra_append_cache(mlra_handle h, void* pool, int num_pages, const int32_t* page_table, int pt_stride,
                       int batch, const int32_t* seq_ids, const int32_t* positions, const void* c_new,
                       const void* kr_new, mlra_dtype in_dtype, int n_tokens, int32_t* status, void* stream) {
@@ -889,6 +959,7 @@ const char* mlra_status_string(int code) {
     case MLRA_ERR_WORKSPACE: return "workspace too small";
     case MLRA_ERR_SEQ_LEN: return "sequence length outside its page-table row";
     case MLRA_ERR_SCRATCH_LIMIT: return "batch needs more than the 16 MiB fixed scratch of mlra_decode_noalloc";
+    case MLRA_ERR_NO_PAGES: return "fewer free pages than the call needs: nothing was changed";
     case MLRA_ERR_DRAIN: return "in-flight device copies or MMAs did not finish after a failed wait: stop using this CUDA context";
     default: return "unknown status";
   }
