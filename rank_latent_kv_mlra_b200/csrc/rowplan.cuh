@@ -163,27 +163,40 @@ struct UnitPart {
   int begin, end;     // key tiles in this stretch (begin < end, or the walk has ended)
   bool valid;
 };
-// Walks the unit parts of a stretch in order. Each role walks on its own, one part ahead of the
-// one it works on, so the plan's reads are not waited for.
+// Walks the unit parts of a stretch in order. One warp calls it (all lanes, same results).
 struct UnitWalk {
   const RowPlan* plan;
-  long long pos, hi;
+  long long pos, hi, at, nx;  // at, nx: where token tile i begins and ends on the line
   int i, tiles, units, key_tile, causal;
-  __device__ __forceinline__ void init(const RowPlan* pl, const Stretch& s, int units_, int key_tile_, int causal_) {
+  TokenTile t;
+  int kv;
+  __device__ __forceinline__ void load() {
+    at = __ldg(plan->start + i);
+    nx = __ldg(plan->start + i + 1);
+    const int4 raw = __ldg(reinterpret_cast<const int4*>(plan->tile + i));
+    t.b = raw.x; t.tok0 = raw.y; t.ntok = raw.z; t.lim0 = raw.w;
+    kv = key_tiles(t, causal, key_tile);
+  }
+  __device__ __forceinline__ void init(const RowPlan* pl, int tiles_, const Stretch& s, int units_, int key_tile_,
+                                       int causal_) {
     plan = pl;
     pos = s.lo;
     hi = s.hi;
     units = units_;
     key_tile = key_tile_;
     causal = causal_;
-    tiles = __ldg(pl->hdr);
-    int lo = 0, up = tiles;  // last tile with start <= pos (zero-cost tiles share a start: the last)
+    tiles = tiles_;
+    // the last tile with start <= pos (tiles without work share their start with the next)
+    int lo = 0, up = tiles;
     while (up - lo > 1) {
-      const int mid = (lo + up) >> 1;
-      if (__ldg(pl->start + mid) <= pos) lo = mid;
-      else up = mid;
+      const int step = (up - lo + 31) / 32, probe = lo + lane_id() * step;
+      const bool in = probe < up && __ldg(pl->start + probe) <= pos;
+      const int n = max(__popc(__ballot_sync(0xffffffffu, in)), 1);
+      lo += (n - 1) * step;
+      up = min(lo + step, up);
     }
     i = lo;
+    if (pos < hi) load();
   }
   __device__ __forceinline__ UnitPart next() {
     UnitPart u;
@@ -191,22 +204,21 @@ struct UnitWalk {
     u.begin = u.end = u.kv = u.sub = 0;
     u.t = {0, 0, 0, 0};
     while (pos < hi) {
-      const long long at = __ldg(plan->start + i), nx = __ldg(plan->start + i + 1);
       if (pos >= nx) {
         ++i;
+        load();
         continue;
       }
-      const int4 raw = __ldg(reinterpret_cast<const int4*>(plan->tile + i));
-      u.t.b = raw.x; u.t.tok0 = raw.y; u.t.ntok = raw.z; u.t.lim0 = raw.w;
-      u.kv = key_tiles(u.t, causal, key_tile);
-      const int cost = unit_cost(u.kv);
-      u.sub = (int)((pos - at) / cost);
+      const int cost = unit_cost(kv);
+      u.sub = (int)((unsigned long long)(pos - at) / (unsigned)cost);
       const long long first = at + (long long)u.sub * cost;
       const long long b = pos - first - kUnitCost, e = hi - first - kUnitCost;
       u.begin = b > 0 ? (int)b : 0;
-      u.end = e < u.kv ? (int)e : u.kv;
+      u.end = e < kv ? (int)e : kv;
       pos = first + cost;
       if (u.end > u.begin) {
+        u.t = t;
+        u.kv = kv;
         u.valid = true;
         return u;
       }

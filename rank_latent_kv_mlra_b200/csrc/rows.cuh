@@ -26,15 +26,64 @@
 
 namespace mlra {
 
-// D(tmem) (+)= A(tmem) * B(smem desc), bf16: A's row r lies in lane r, two K elements a column.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// One lane of a converged warp; the same one each time. The MMA warp runs its loops whole, and only
+// the instructions that must come from one thread sit behind this predicate, so descriptors stay in
+// uniform registers (with the loops themselves behind a lane test an MMA took 86 clocks to issue).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// Shared-memory descriptors as two words (see smem_desc): the upper word is the same for all tiles of a
+// layout, the lower one moves by offset / 16.
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t layout) {
+  return ((sbo >> 4) & 0x3FFFu) | (1u << 14) | (layout << 29);
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
+}
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// A from tensor memory: its row r lies in lane r, two K elements a column.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A warpgroup's share of the block's registers (every warp of it executes this).
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// The largest of three; NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void fma_f32x2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0,
+                                          float c1) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(f2pack(a0, a1)), "l"(f2pack(b0, b1)), "l"(f2pack(c0, c1)));
+  d0 = __uint_as_float(static_cast<uint32_t>(d));
+  d1 = __uint_as_float(static_cast<uint32_t>(d >> 32));
 }
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
                                             int w, uint64_t policy) {
@@ -68,12 +117,18 @@ struct RowShape {
   static constexpr int O_COL = NQ * SB * KT;
   static constexpr int TMEM_USED = O_COL + NQ * DV;
   static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
-  static constexpr int MMA_WARP = 4 * NQ, LOAD_WARP = MMA_WARP + 1, FIX_WARP = MMA_WARP + 2;
-  static constexpr int THREADS = 32 * (FIX_WARP + 1);
-  static constexpr int NBARS = 2 * STAGES + 2 + 2 * NQ * SB + 2 * NQ + 4;
+  static constexpr int MMA_WARP = 4 * NQ, LOAD_WARP = MMA_WARP + 1, FIX_WARP = MMA_WARP + 2, WALK_WARP = MMA_WARP + 3;
+  static constexpr int THREADS = 32 * (WALK_WARP + 1);
+  // Two row tiles: 384 threads are launched with 168 registers each (64,512); the two softmax
+  // warpgroups take 208 (53,248) and the other one keeps 88 (11,264).
+  static constexpr bool REGS = NQ == 2;
+  static constexpr int PARTS = 4;            // unit parts handed out ahead
+  static constexpr int READERS = 4 * NQ + 3; // warps that read them
+  static constexpr int NBARS = 2 * STAGES + 2 + 2 * NQ * SB + 2 * NQ + 4 + 2 * PARTS;
   static constexpr int OFF_STAGES = NQ * Q_BYTES;
   static constexpr int OFF_BAR = OFF_STAGES + STAGES * STAGE_BYTES;
-  static constexpr int SMEM = OFF_BAR + NBARS * 8 + 64 + 1024;
+  static constexpr int OFF_PARTS = (OFF_BAR + NBARS * 8 + 15) / 16 * 16;
+  static constexpr int SMEM = OFF_PARTS + PARTS * 48 + 64 + 1024;
   static_assert(SMEM <= 227 * 1024 && TMEM_USED <= 512, "shared and tensor memory of one CTA");
   static_assert(KT == 64 || KT == 128, "whole pages");
   static_assert(DV <= 256 && DV % 16 == 0 && DB % DV == 0, "one PV instruction's columns");
@@ -92,6 +147,7 @@ struct RowParams {
   int tok_tile;            // tokens of a row tile: 128 / heads_tile
   int heads_block, vh;     // heads of a block, (virtual) heads in all
   int d_c;
+  float s_scale;           // from a score (packed query times staged row) to log2 units
   float o_scale;           // value of a staged latent element (1, or the E4M3 cache's scale)
   __nv_bfloat16* o_bf16;   // [tokens][vh][DB], or null
   float* o_f32;            // [tokens][vh][DB] when o_bf16 is null
@@ -129,7 +185,10 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
   uint64_t* patch = pvdone + 1;          // a key tile is ready to be patched
   uint64_t* patched_bar = patch + 1;     // and has been
   uint64_t* drained = patched_bar + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Sh::NBARS);
+  uint64_t* pready = drained + 1;        // [PARTS]
+  uint64_t* pread = pready + Sh::PARTS;  // [PARTS]
+  int4* parts = reinterpret_cast<int4*>(smem + Sh::OFF_PARTS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(parts + 3 * Sh::PARTS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* drain_err = abort_flag + 1;
 
@@ -153,6 +212,10 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
     mbar_init(patch, 1);
     mbar_init(patched_bar, 1);
     mbar_init(drained, 1);
+    for (int i = 0; i < Sh::PARTS; ++i) {
+      mbar_init(&pready[i], 1);
+      mbar_init(&pread[i], Sh::READERS);
+    }
     *abort_flag = 0;
     *drain_err = 0;
     fence_mbar_init();
@@ -176,34 +239,46 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
   const uint32_t tbase = *tmem_slot;
   grid_launch_dependents();
 
-  const int units = p.nsub * Sh::HALVES;
-  const Stretch st = stretch_of(__ldg(p.plan.start + __ldg(p.plan.hdr)), blockIdx.x, gridDim.x);
-  UnitWalk walk;
-  walk.init(&p.plan, st, units, KT, p.causal);
-  UnitPart nx = walk.next();
-
   uint32_t kt = 0;    // key tiles so far (stage ring)
   uint32_t uc = 0;    // unit parts so far
   uint32_t fc = 0;    // key tiles that were patched so far
+  auto wait = [&](uint64_t* b, uint32_t par) {
+    return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, p.wait_limit_ns));
+  };
+  // the next unit part from the walk warp's ring; false after the last one
+  auto take = [&](UnitPart& u) {
+    const int e = uc % Sh::PARTS;
+    if (!wait(&pready[e], (uc / Sh::PARTS) & 1)) return false;
+    const int4 a = parts[3 * e], b = parts[3 * e + 1];
+    u.valid = parts[3 * e + 2].x != 0;
+    u.t = {a.x, a.y, a.z, a.w};
+    u.sub = b.x; u.kv = b.y; u.begin = b.z; u.end = b.w;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&pread[e]);
+    ++uc;
+    return u.valid;
+  };
+  UnitPart u;
 
+  // (the register split sits in the two branches, so that each is compiled for its own share)
+  if (warp >= 4 * NQ) {
+  if constexpr (Sh::REGS) regs_down<88>();
   if (warp == Sh::LOAD_WARP) {
     // ------------------------------ TMA loads ------------------------------
     const uint64_t pol = l2_policy_evict_last();
     uint32_t issued = 0, parity = 0;
     int q_parity = -1;  // of the last query load
     bool ok = true;
-    while (nx.valid && ok) {
-      const UnitPart u = nx;
-      nx = walk.next();
+    while (ok && take(u)) {
       const int sub = u.sub / Sh::HALVES;
       const int blk = sub / p.chunks;
       const int nrow = u.t.ntok > p.tok_tile ? NQ : 1;  // row tiles in use
       if (lane == 0) {
-        ok = mbar_wait(qempty, (uc & 1) ^ 1, abort_flag, p.wait_limit_ns);
+        ok = mbar_wait(qempty, uc & 1, abort_flag, p.wait_limit_ns);
         if (ok) {
           const int rows = p.heads_tile * p.tok_tile;
           mbar_arrive_expect_tx(qfull, nrow * rows * (Sh::DB + Sh::DR) * 2);
-          q_parity = uc & 1;
+          q_parity = (uc - 1) & 1;
           for (int q = 0; q < nrow; ++q) {
             uint8_t* dst = qbuf + q * Sh::Q_BYTES;
             const int tok = u.t.tok0 + q * p.tok_tile;
@@ -266,7 +341,6 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      ++uc;
     }
     if (lane == 0) {
       // nothing may still be landing when the CTA's shared memory is released
@@ -277,122 +351,119 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
     }
   } else if (warp == Sh::MMA_WARP) {
     // ------------------------------ MMAs ------------------------------
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, KT, false, false);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV, false, true);
-      const uint32_t q_addr = smem_u32(qbuf), k_addr = smem_u32(stages);
-      auto issue_qk = [&](int q, uint32_t tile) {
-        const uint32_t a0 = q_addr + q * Sh::Q_BYTES, b0 = k_addr + (tile % STAGES) * Sh::STAGE_BYTES;
-        const uint32_t sbuf = q * SB + (SB == 2 ? tile & 1 : 0);
-        const uint32_t d = tbase + Sh::S_COL + sbuf * KT;
+    const bool one = elect_lane();
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, KT, false, false);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV, false, true);
+    constexpr uint32_t c_hi = desc_hi(8 * Sh::C_ROWB, swizzle_code(Sh::C_ROWB));
+    constexpr uint32_t r_hi = desc_hi(8 * Sh::R_ROWB, swizzle_code(Sh::R_ROWB));
+    const uint32_t q_lo = desc_lo(smem_u32(qbuf), 16), k_lo = desc_lo(smem_u32(stages), 16);
+    const uint32_t v_lo = desc_lo(smem_u32(stages), Sh::KC_REG);
+    auto issue_qk = [&](int q, uint32_t tile) {
+      const uint32_t a0 = q_lo + q * (Sh::Q_BYTES >> 4), b0 = k_lo + (tile % STAGES) * (Sh::STAGE_BYTES >> 4);
+      const uint32_t sbuf = q * SB + (SB == 2 ? tile & 1 : 0);
+      const uint32_t d = tbase + Sh::S_COL + sbuf * KT;
+      if (one) {
 #pragma unroll
         for (int r = 0; r < Sh::NC; ++r)
 #pragma unroll
           for (int ks = 0; ks < Sh::C_ROWB / 32; ++ks)
-            umma_bf16(d, smem_desc(a0 + r * Sh::QC_REG + ks * 32, 16, 8 * Sh::C_ROWB, swizzle_code(Sh::C_ROWB)),
-                      smem_desc(b0 + r * Sh::KC_REG + ks * 32, 16, 8 * Sh::C_ROWB, swizzle_code(Sh::C_ROWB)), idesc_qk,
-                      (r > 0 || ks > 0) ? 1u : 0u);
+            umma_ss(d, a0 + ((r * Sh::QC_REG + ks * 32) >> 4), c_hi, b0 + ((r * Sh::KC_REG + ks * 32) >> 4), c_hi,
+                    idesc_qk, (r > 0 || ks > 0) ? 1u : 0u);
 #pragma unroll
         for (int r = 0; r < Sh::NR; ++r)
 #pragma unroll
           for (int ks = 0; ks < Sh::R_ROWB / 32; ++ks)
-            umma_bf16(d,
-                      smem_desc(a0 + Sh::NC * Sh::QC_REG + r * Sh::QR_REG + ks * 32, 16, 8 * Sh::R_ROWB,
-                                swizzle_code(Sh::R_ROWB)),
-                      smem_desc(b0 + Sh::NC * Sh::KC_REG + r * Sh::KR_REG + ks * 32, 16, 8 * Sh::R_ROWB,
-                                swizzle_code(Sh::R_ROWB)),
-                      idesc_qk, 1u);
+            umma_ss(d, a0 + ((Sh::NC * Sh::QC_REG + r * Sh::QR_REG + ks * 32) >> 4), r_hi,
+                    b0 + ((Sh::NC * Sh::KC_REG + r * Sh::KR_REG + ks * 32) >> 4), r_hi, idesc_qk, 1u);
         umma_commit(&sfull[sbuf]);
-      };
-      auto issue_pv = [&](int q, uint32_t tile, int half, bool first) {
-        const uint32_t b0 = k_addr + (tile % STAGES) * Sh::STAGE_BYTES + half * (DV / Sh::CW) * Sh::KC_REG;
-        const uint32_t sbuf = q * SB + (SB == 2 ? tile & 1 : 0);
-        const uint32_t a = tbase + Sh::S_COL + sbuf * KT;
+      }
+    };
+    auto issue_pv = [&](int q, uint32_t tile, int half, bool first) {
+      const uint32_t b0 = v_lo + (tile % STAGES) * (Sh::STAGE_BYTES >> 4) + half * ((DV / Sh::CW) * (Sh::KC_REG >> 4));
+      const uint32_t sbuf = q * SB + (SB == 2 ? tile & 1 : 0);
+      const uint32_t a = tbase + Sh::S_COL + sbuf * KT;
+      if (one) {
 #pragma unroll
         for (int ks = 0; ks < KT / 16; ++ks)
-          umma_bf16_ts(tbase + Sh::O_COL + q * DV, a + ks * 8,
-                       smem_desc(b0 + ks * 16 * Sh::C_ROWB, Sh::KC_REG, 8 * Sh::C_ROWB, swizzle_code(Sh::C_ROWB)),
-                       idesc_pv, (first && ks == 0) ? 0u : 1u);
-      };
-      auto wait = [&](uint64_t* b, uint32_t par) { return mbar_wait(b, par, abort_flag, p.wait_limit_ns); };
-      uint32_t pc[NQ];  // score tiles so far, a row tile
+          umma_ts(tbase + Sh::O_COL + q * DV, a + ks * 8, b0 + ((ks * 16 * Sh::C_ROWB) >> 4), c_hi, idesc_pv,
+                  (first && ks == 0) ? 0u : 1u);
+      }
+    };
+    auto commit = [&](uint64_t* b) {
+      if (one) umma_commit(b);
+    };
+    uint32_t pc[NQ];  // score tiles so far, a row tile
+    uint32_t oc[NQ];  // parts so far, a row tile
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) pc[q] = 0;
-      uint32_t oc[NQ];  // parts so far, a row tile
+    for (int q = 0; q < NQ; ++q) pc[q] = oc[q] = 0;
+    bool ok = true;
+    while (ok && take(u)) {
+      const int half = u.sub % Sh::HALVES;
+      const int nrow = NQ == 2 && u.t.ntok > p.tok_tile ? 2 : 1;
+      const int n = u.end - u.begin;
+      ok = wait(qfull, (uc - 1) & 1) && wait(&kfull[kt % STAGES], (kt / STAGES) & 1);
+      if (!ok) break;
+      tc_fence_after();
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) oc[q] = 0;
-      bool ok = true;
-      while (nx.valid && ok) {
-        const UnitPart u = nx;
-        nx = walk.next();
-        const int half = u.sub % Sh::HALVES;
-        const int nrow = NQ == 2 && u.t.ntok > p.tok_tile ? 2 : 1;
-        const int n = u.end - u.begin;
-        ok = wait(qfull, uc & 1) && wait(&kfull[kt % STAGES], (kt / STAGES) & 1);
-        if (!ok) break;
+      for (int q = 0; q < NQ; ++q)
+        if (q < nrow) issue_qk(q, kt);
+      // a tile that reaches past what the unit's first token sees is patched (see the patch
+      // warp) between its score MMAs and its value MMAs
+      auto patched = [&](int i) { return (u.begin + i + 1) * KT > u.t.lim0; };
+      if (patched(0)) commit(patch);
+      if (n == 1) commit(qempty);
+      // the next tile's scores go out before this tile's values where a second stage holds it
+      auto next_qk = [&](int i) {
+        if (i + 1 >= n) return true;
+        const uint32_t tile = kt + i + 1;
+        if (!wait(&kfull[tile % STAGES], (tile / STAGES) & 1)) return false;
         tc_fence_after();
+        issue_qk(0, tile);
+        if (patched(i + 1)) commit(patch);
+        if (i + 2 == n) commit(qempty);
+        return true;
+      };
+      for (int i = 0; i < n && ok; ++i) {
+        const uint32_t tile = kt + i;
+        if (NQ == 1 && STAGES > 1) ok = next_qk(i);
 #pragma unroll
-        for (int q = 0; q < NQ; ++q)
-          if (q < nrow) issue_qk(q, kt);
-        // a tile that reaches past what the unit's first token sees is patched (see the patch
-        // warp) between its score MMAs and its value MMAs
-        auto patched = [&](int i) { return (u.begin + i + 1) * KT > u.t.lim0; };
-        if (patched(0)) umma_commit(patch);
-        if (n == 1) umma_commit(qempty);
-        // the next tile's scores go out before this tile's values where a second stage holds it
-        auto next_qk = [&](int i) {
-          if (i + 1 >= n) return true;
-          const uint32_t tile = kt + i + 1;
-          if (!wait(&kfull[tile % STAGES], (tile / STAGES) & 1)) return false;
+        for (int q = 0; q < NQ; ++q) {
+          if (q >= nrow || !ok) break;
+          const uint32_t pb = q * SB + (SB == 2 ? tile & 1 : 0);
+          const uint32_t pph = SB == 2 ? (tile >> 1) & 1 : pc[q] & 1;
+          ok = wait(&pfull[pb], pph);
+          if (ok && q == 0 && patched(i)) ok = wait(patched_bar, fc & 1);
+          if (ok && i == 0) ok = wait(&ofree[q], (oc[q] & 1) ^ 1);
+          if (!ok) break;
+          ++pc[q];
           tc_fence_after();
-          issue_qk(0, tile);
-          if (patched(i + 1)) umma_commit(patch);
-          if (i + 2 == n) umma_commit(qempty);
-          return true;
-        };
-        for (int i = 0; i < n && ok; ++i) {
-          const uint32_t tile = kt + i;
-          if (NQ == 1 && STAGES > 1) ok = next_qk(i);
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            if (q >= nrow || !ok) break;
-            const uint32_t pb = q * SB + (SB == 2 ? tile & 1 : 0);
-            const uint32_t pph = SB == 2 ? (tile >> 1) & 1 : pc[q] & 1;
-            ok = wait(&pfull[pb], pph);
-            if (ok && q == 0 && patched(i)) ok = wait(patched_bar, fc & 1);
-            if (ok && i == 0) ok = wait(&ofree[q], (oc[q] & 1) ^ 1);
-            if (!ok) break;
-            ++pc[q];
-            tc_fence_after();
-            issue_pv(q, tile, half, i == 0);
-            if (q == nrow - 1) umma_commit(&kempty[tile % STAGES]);
-            if (NQ == 1) umma_commit(pvdone);
-            if (i == n - 1) {
-              umma_commit(&ofull[q]);
-              ++oc[q];
+          issue_pv(q, tile, half, i == 0);
+          if (q == nrow - 1) commit(&kempty[tile % STAGES]);
+          if (NQ == 1) commit(pvdone);
+          if (i == n - 1) {
+            commit(&ofull[q]);
+            ++oc[q];
+          }
+          if (NQ == 2 && i + 1 < n) {
+            if (q == 0) {
+              ok = wait(&kfull[(tile + 1) % STAGES], ((tile + 1) / STAGES) & 1);
+              if (!ok) break;
+              tc_fence_after();
             }
-            if (NQ == 2 && i + 1 < n) {
-              if (q == 0) {
-                ok = wait(&kfull[(tile + 1) % STAGES], ((tile + 1) / STAGES) & 1);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              issue_qk(q, tile + 1);
-              if (q == nrow - 1) {
-                if (patched(i + 1)) umma_commit(patch);
-                if (i + 2 == n) umma_commit(qempty);
-              }
+            issue_qk(q, tile + 1);
+            if (q == nrow - 1) {
+              if (patched(i + 1)) commit(patch);
+              if (i + 2 == n) commit(qempty);
             }
           }
-          if (patched(i)) ++fc;
-          if (NQ == 1 && STAGES == 1 && ok) ok = next_qk(i);
         }
-        kt += n;
-        ++uc;
+        if (patched(i)) ++fc;
+        if (NQ == 1 && STAGES == 1 && ok) ok = next_qk(i);
       }
-      umma_commit(drained);
-      if (!mbar_wait_drain(drained, 0, p.wait_limit_ns)) *drain_err = 1;
+      kt += n;
     }
+    commit(drained);
+    if (!mbar_wait_drain(drained, 0, p.wait_limit_ns)) *drain_err = 1;
     __syncwarp();
   } else if (warp == Sh::FIX_WARP) {
     // ------------------------------ patches ------------------------------
@@ -402,16 +473,12 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
     // its tokens see are zeroed where they are not finite. A token that does see such a row gets
     // its NaN through the score, whose MMA has read the tile before it is patched.
     bool ok = true;
-    while (nx.valid && ok) {
-      const UnitPart u = nx;
-      nx = walk.next();
+    while (ok && take(u)) {
       const int lim = tile_limit(u.t, p.causal);
       for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
         if ((t + 1) * KT > u.t.lim0) {
           // the MMAs that form this key tile's scores have read it (and it had landed)
-          ok = mbar_wait(patch, fc & 1, abort_flag, p.wait_limit_ns) &&
-               mbar_wait(&kfull[kt % STAGES], (kt / STAGES) & 1, abort_flag, p.wait_limit_ns);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = wait(patch, fc & 1) && wait(&kfull[kt % STAGES], (kt / STAGES) & 1);
           if (!ok) break;
           ++fc;
           uint8_t* st_mem = stages + (kt % STAGES) * Sh::STAGE_BYTES;
@@ -441,7 +508,28 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         }
       }
     }
+  } else if (warp == Sh::WALK_WARP) {
+    // ------------------------------ the walk ------------------------------
+    const int tiles = __ldg(p.plan.hdr);
+    UnitWalk walk;
+    walk.init(&p.plan, tiles, stretch_of(__ldg(p.plan.start + tiles), blockIdx.x, gridDim.x), p.nsub * Sh::HALVES, KT,
+              p.causal);
+    do {
+      u = walk.next();
+      const int e = uc % Sh::PARTS;
+      if (!wait(&pread[e], ((uc / Sh::PARTS) & 1) ^ 1)) break;
+      if (lane == 0) {
+        parts[3 * e] = make_int4(u.t.b, u.t.tok0, u.t.ntok, u.t.lim0);
+        parts[3 * e + 1] = make_int4(u.sub, u.kv, u.begin, u.end);
+        parts[3 * e + 2].x = u.valid;
+        mbar_arrive(&pready[e]);
+      }
+      __syncwarp();
+      ++uc;
+    } while (u.valid);
+  }
   } else {
+    if constexpr (Sh::REGS) regs_up<208>();
     // ------------------------------ softmax and results ------------------------------
     // A thread owns one row. The running maximum is raised only when a score passes it by more
     // than 8 (log2 units), so P stays below 2^8 and O is rescaled in tensor memory only then.
@@ -454,9 +542,8 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
     const bool row_in = tl < p.tok_tile;
     uint32_t sc = 0, oc = 0;
     bool ok = true;
-    while (nx.valid && ok) {
-      const UnitPart u = nx;
-      nx = walk.next();
+    const float sc_mul = p.s_scale, slack = 8.f / sc_mul;
+    while (ok && take(u)) {
       const int n = u.end - u.begin;
       if (q > 0 && u.t.ntok <= p.tok_tile) {
         kt += n;
@@ -467,7 +554,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       for (int i = 0; i < n; ++i, ++kt, ++sc) {
         const uint32_t sb = q * SB + (SB == 2 ? kt & 1 : 0);
         const uint32_t par = SB == 2 ? (kt >> 1) & 1 : sc & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[sb], par, abort_flag, p.wait_limit_ns));
+        ok = wait(&sfull[sb], par);
         if (!ok) break;
         tc_fence_after();
         const uint32_t s_addr = tbase + lane_base + Sh::S_COL + sb * KT;
@@ -481,29 +568,27 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         }
         float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
 #pragma unroll
-        for (int c = 4; c < KT; c += 4) {
-          x0 = fmaxf(x0, s[c]);
-          x1 = fmaxf(x1, s[c + 1]);
-          x2 = fmaxf(x2, s[c + 2]);
-          x3 = fmaxf(x3, s[c + 3]);
+        for (int c = 4; c + 8 <= KT; c += 8) {
+          x0 = max3_nan(x0, s[c], s[c + 1]);
+          x1 = max3_nan(x1, s[c + 2], s[c + 3]);
+          x2 = max3_nan(x2, s[c + 4], s[c + 5]);
+          x3 = max3_nan(x3, s[c + 6], s[c + 7]);
         }
-        const float mt = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+        x0 = max3_nan(x0, s[KT - 4], s[KT - 3]);
+        x1 = max3_nan(x1, s[KT - 2], s[KT - 1]);
+        const float mt = max3_nan(max3_nan(x0, x1, x2), x3, x3);
         if (i == 0) {
           m = mt;
         } else {
-          const bool raise = mt > m + 8.f;
+          const bool raise = mt > m + slack;
           if (__any_sync(0xffffffffu, raise)) {
             // with one score buffer this tile's scores were issued after the last PV; with two the
             // last PV has its own barrier
             // (waited for from the phase before it, so that the parity is that phase's)
-            if (NQ == 1) {
-              ok = kt < 2 || mbar_wait(pvdone, kt & 1, abort_flag, p.wait_limit_ns);
-              ok = ok && mbar_wait(pvdone, (kt - 1) & 1, abort_flag, p.wait_limit_ns);
-              ok = __all_sync(0xffffffffu, ok);
-            }
+            if (NQ == 1) ok = (kt < 2 || wait(pvdone, kt & 1)) && wait(pvdone, (kt - 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            const float a = raise ? fast_exp2(m - mt) : 1.f;
+            const float a = raise ? fast_exp2((m - mt) * sc_mul) : 1.f;
             l *= a;
             if (raise) m = mt;
 #pragma unroll 1
@@ -518,33 +603,31 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
             tmem_st_wait();
           }
         }
-        const float mu = m == -INFINITY ? 0.f : m;  // a row that sees no key of this part: P = 0
-        float l0 = 0.f, l1 = 0.f;
-        uint32_t pk[KT / 2];
+        const float mu = m == -INFINITY ? 0.f : -m * sc_mul;  // a row that sees no key of this part: P = 0
+        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
-        for (int c = 0; c < KT; c += 2) {
-          float e0, e1;
-          sub_f32x2(e0, e1, s[c], s[c + 1], mu, mu);
-          e0 = fast_exp2(e0);
-          e1 = fast_exp2(e1);
-          add_f32x2(l0, l1, l0, l1, e0, e1);
-          pk[c / 2] = pack_bf16x2(e0, e1);  // P to bf16 (half a step 2^-9) for the tensor core
+        for (int c0 = 0; c0 < KT; c0 += 64) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            float e0, e1;
+            fma_f32x2(e0, e1, s[c0 + c], s[c0 + c + 1], sc_mul, sc_mul, mu, mu);
+            e0 = fast_exp2(e0);
+            e1 = fast_exp2(e1);
+            if (c & 2) add_f32x2(l2, l3, l2, l3, e0, e1);
+            else add_f32x2(l0, l1, l0, l1, e0, e1);
+            pk[c / 2] = pack_bf16x2(e0, e1);  // P to bf16 (half a step 2^-8 relative) for the tensor core
+          }
+          tmem_st32(s_addr + c0 / 2, pk);
         }
-        l += l0 + l1;
-#pragma unroll
-        for (int c = 0; c < KT / 2; c += 32) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = pk[c + e];
-          tmem_st32(s_addr + c, w);
-        }
+        l += (l0 + l1) + (l2 + l3);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[sb]);
       }
       if (!ok) break;
-      ok = __all_sync(0xffffffffu, mbar_wait(&ofull[q], oc & 1, abort_flag, p.wait_limit_ns));
+      ok = wait(&ofull[q], oc & 1);
       if (!ok) break;
       ++oc;
       tc_fence_after();
@@ -555,7 +638,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       const bool whole = u.begin == 0 && u.end == u.kv;
       const int slot = 2 * blockIdx.x + (u.begin == 0 ? 1 : 0);
       const float inv = l > 0.f ? p.o_scale / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
-      const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
+      const float lse2 = l == 0.f ? -INFINITY : m * sc_mul + __log2f(l);
       const size_t at = (size_t)(u.t.tok0 + tok) * p.vh + head;
       const size_t pat = (size_t)slot * Sh::ROWS + q * 128 + row;
       if (mine && half == 0) {

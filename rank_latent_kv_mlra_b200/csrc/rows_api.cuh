@@ -312,8 +312,7 @@ ProjParams absorb_params(const mlra_ctx* h, const void* q, mlra_dtype q_dtype, i
   pp.q = q;
   pp.q_f32 = q_dtype == MLRA_F32;
   pp.q_pack = q_pack;
-  pp.qscale = h->scale * kLog2e * (h->fp8 ? h->latent_scale : 1.f);
-  pp.qscale_rope = h->scale * kLog2e * (h->fp8 ? h->rope_scale : 1.f);
+  pp.qscale = pp.qscale_rope = h->scale * kLog2e;
   pp.d_r = h->d_r;
   pp.np = h->np;
   pp.nsub = h->nsub;
@@ -358,7 +357,11 @@ int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t*
     return cudaMemsetAsync(w.status, 0, 4, s) == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
 
   const EarlyTags tags = {reinterpret_cast<unsigned*>(w.status) + 1, next_call_tag()};
-  const ProjParams pp = absorb_params(h, q, q_dtype, total_q, w.q_pack, w.status, tags);
+  ProjParams pp = absorb_params(h, q, q_dtype, total_q, w.q_pack, w.status, tags);
+  // The scores are scaled in the softmax, so that q^R goes in as it is (a bf16 query's is not
+  // rounded again); an E4M3 cache's latent scale goes into q~ relative to the RoPE scale.
+  pp.qscale = h->fp8 ? h->latent_scale / h->rope_scale : 1.f;
+  pp.qscale_rope = 1.f;
   RowsCall c = {};
   c.q_pack = w.q_pack;
   c.tokens = total_q;
@@ -371,6 +374,7 @@ int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t*
   c.pt_stride = pt_stride;
   c.causal = true;
   c.rp.plan = w.rows.plan;
+  c.rp.s_scale = h->scale * kLog2e * (h->fp8 ? h->rope_scale : 1.f);
   c.rp.o_scale = h->fp8 ? h->latent_scale : 1.f;
   c.rp.o_bf16 = w.o;
   c.rp.lse = lse;
@@ -451,6 +455,7 @@ int run_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const vo
   c.pt_stride = prefix_stride;
   c.causal = false;
   c.rp.plan = w.rows.plan;
+  c.rp.s_scale = 1.f;
   c.rp.o_scale = 1.f;
   c.rp.o_f32 = w.o;
   c.rp.lse = w.lse;

@@ -209,7 +209,11 @@ def test_prefill_then_decode_agree_on_the_last_token():
     M.mlra_decode(hdl, inp["q"], inp["pool"], inp["page_table"], inp["seq_lens"], dout, dlse)
     torch.cuda.synchronize()
     G.assert_parity(out.cpu().numpy(), dout.double().cpu().numpy(), "prefill against decode")
-    assert (lse - dlse).abs().max() < 1e-3
+    # The two round the absorbed query differently (the decode step scales it first). A score moves by
+    # a sum of independent roundings of at most half a bf16 step, 2^-8 relative: rms at most
+    # 2^-8 / sqrt(3) of a score's own rms 1; an lse moves by an average of its scores' errors, so
+    # by less than the largest: 4 sigma, two sides.
+    assert (lse - dlse).abs().max() < 4 * 2 ** 0.5 * 2 ** -8 / 3 ** 0.5
 
 
 def test_large_scores_raise_the_running_maximum():
