@@ -98,12 +98,18 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // The attention kernel
 // ---------------------------------------------------------------------------------------
 // DB, DR: block and RoPE widths; KT: keys a tile (64 or 128); DV: value columns a CTA keeps
-// (DB, or a half of it where DB fp32 columns would fill the tensor memory); NQ row tiles in turn;
-// SB score buffers a row tile (NQ = 1 hides the softmax behind the next tile's scores instead).
-template <int DB_, int DR_, int KT_, int DV_, int NQ_, int STAGES_>
+// (DB, or a half of it where DB fp32 columns would fill the tensor memory); NQ row tiles in turn.
+// A key tile is staged as its block columns (ring of CST) and its RoPE columns (ring of RST): the
+// scores of both row tiles are formed early, after which the RoPE columns are done with, while the
+// block columns wait for both P. At d_b = 128 that is what lets three tiles' block columns fit.
+// Tensor memory: with two row tiles, one score buffer that they use in turn (a softmax warpgroup has
+// it in registers about 200 clocks after it is ready, so the next scores are formed while the
+// exponentials run) and a P buffer each; with one, two score buffers and one P buffer.
+// Scores and values are issued by two warps: an MMA holds its issuer up while the tensor pipe's short
+// queue is full, and each wait costs a few hundred clocks, which one warp's MMAs hide for the other.
+template <int DB_, int DR_, int KT_, int DV_, int NQ_, int CST_, int RST_>
 struct RowShape {
-  static constexpr int DB = DB_, DR = DR_, KT = KT_, DV = DV_, NQ = NQ_, STAGES = STAGES_;
-  static constexpr int SB = NQ == 1 ? 2 : 1;
+  static constexpr int DB = DB_, DR = DR_, KT = KT_, DV = DV_, NQ = NQ_, CST = CST_, RST = RST_;
   static constexpr int HALVES = DB / DV;
   static constexpr int ROWS = 128 * NQ;     // query rows a unit
   static constexpr int CW = DB < 64 ? DB : 64, NC = DB / CW, C_ROWB = CW * 2;
@@ -111,29 +117,34 @@ struct RowShape {
   static constexpr int QC_REG = 128 * C_ROWB, QR_REG = 128 * R_ROWB;
   static constexpr int Q_BYTES = NC * QC_REG + NR * QR_REG;
   static constexpr int KC_REG = KT * C_ROWB, KR_REG = KT * R_ROWB;
-  static constexpr int STAGE_BYTES = NC * KC_REG + NR * KR_REG;
+  static constexpr int C_BYTES = NC * KC_REG, R_BYTES = NR * KR_REG;
   static constexpr int PAGE_TX = kPage * (DB + DR) * 2;
-  static constexpr int S_COL = 0;                       // NQ * SB buffers of KT columns
-  static constexpr int O_COL = NQ * SB * KT;
+  static constexpr int SB = NQ == 1 ? 2 : 1;                  // score buffers
+  static constexpr int S_COL = 0;
+  static constexpr int P_COL = SB * KT;                       // KT / 2 columns a row tile
+  static constexpr int O_COL = P_COL + NQ * (KT / 2);
   static constexpr int TMEM_USED = O_COL + NQ * DV;
   static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
-  static constexpr int MMA_WARP = 4 * NQ, LOAD_WARP = MMA_WARP + 1, FIX_WARP = MMA_WARP + 2, WALK_WARP = MMA_WARP + 3;
-  static constexpr int THREADS = 32 * (WALK_WARP + 1);
+  static constexpr int QK_WARP = 4 * NQ, PV_WARP = QK_WARP + 1, LOAD_WARP = QK_WARP + 2, FIX_WARP = QK_WARP + 3;
+  static constexpr int THREADS = 32 * (FIX_WARP + 1);
   // Two row tiles: 384 threads are launched with 168 registers each (64,512); the two softmax
   // warpgroups take 208 (53,248) and the other one keeps 88 (11,264).
   static constexpr bool REGS = NQ == 2;
   static constexpr int PARTS = 4;            // unit parts handed out ahead
-  static constexpr int READERS = 4 * NQ + 3; // warps that read them
-  static constexpr int NBARS = 2 * STAGES + 2 + 2 * NQ * SB + 2 * NQ + 4 + 2 * PARTS;
-  static constexpr int OFF_STAGES = NQ * Q_BYTES;
-  static constexpr int OFF_BAR = OFF_STAGES + STAGES * STAGE_BYTES;
+  static constexpr int READERS = 4 * NQ + 4; // warps that read them
+  static constexpr int NBARS = 4 * CST + RST + 2 * NQ + 4 + 3 * NQ + 2 + 2 * PARTS;
+  static constexpr int OFF_C = NQ * Q_BYTES;
+  static constexpr int OFF_R = OFF_C + CST * C_BYTES;
+  static constexpr int OFF_BAR = OFF_R + RST * R_BYTES;
   static constexpr int OFF_PARTS = (OFF_BAR + NBARS * 8 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_PARTS + PARTS * 48 + 64 + 1024;
   static_assert(SMEM <= 227 * 1024 && TMEM_USED <= 512, "shared and tensor memory of one CTA");
   static_assert(KT == 64 || KT == 128, "whole pages");
   static_assert(DV <= 256 && DV % 16 == 0 && DB % DV == 0, "one PV instruction's columns");
-  static_assert(Q_BYTES % 1024 == 0 && STAGE_BYTES % 1024 == 0 && KC_REG % 1024 == 0 && QC_REG % 1024 == 0,
+  static_assert(Q_BYTES % 1024 == 0 && C_BYTES % 1024 == 0 && R_BYTES % 1024 == 0 && KC_REG % 1024 == 0 &&
+                    QC_REG % 1024 == 0 && KR_REG % 1024 == 0 && QR_REG % 1024 == 0,
                 "swizzled regions start on 1024 bytes");
+  static_assert(RST <= CST && (NQ == 1 || CST >= 2), "a tile's full barrier counts both rings");
 };
 
 struct RowParams {
@@ -159,6 +170,27 @@ struct RowParams {
   unsigned long long wait_limit_ns;
 };
 
+// Four lanes that hold four 16-byte pieces of their own rows each exchange them, so that lane j ends
+// with piece j of all four rows: a store then covers 64 bytes in a row instead of 16.
+__device__ __forceinline__ void exchange4(uint4 (&v)[4], int lane) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      if (p & o) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t a = w[p * 4 + e], b = w[(p | o) * 4 + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, o);
+        w[p * 4 + e] = up ? got : a;
+        w[(p | o) * 4 + e] = up ? b : got;
+      }
+    }
+  }
+}
+
 // A unit cut by the stretches leaves CTA c's part in slot 2c + 1 where the part begins the unit,
 // in slot 2c where it goes on with one begun before (a stretch holds at most one of each).
 template <class Sh>
@@ -166,26 +198,29 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
     mlra_rows_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_r,
                      const __grid_constant__ CUtensorMap map_qc, const __grid_constant__ CUtensorMap map_qr,
                      const RowParams p) {
-  constexpr int NQ = Sh::NQ, SB = Sh::SB, KT = Sh::KT, STAGES = Sh::STAGES, DV = Sh::DV;
+  constexpr int NQ = Sh::NQ, KT = Sh::KT, CST = Sh::CST, RST = Sh::RST, DV = Sh::DV;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* qbuf = smem;
-  uint8_t* stages = smem + Sh::OFF_STAGES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::OFF_BAR);
-  uint64_t* kfull = bars;
-  uint64_t* kempty = kfull + STAGES;
-  uint64_t* qfull = kempty + STAGES;
-  uint64_t* qempty = qfull + 1;
-  uint64_t* sfull = qempty + 1;          // [NQ * SB]
-  uint64_t* pfull = sfull + NQ * SB;     // [NQ * SB]
-  uint64_t* ofull = pfull + NQ * SB;     // [NQ]
-  uint64_t* ofree = ofull + NQ;          // [NQ]
-  uint64_t* pvdone = ofree + NQ;         // NQ = 1 only
-  uint64_t* patch = pvdone + 1;          // a key tile is ready to be patched
-  uint64_t* patched_bar = patch + 1;     // and has been
-  uint64_t* drained = patched_bar + 1;
-  uint64_t* pready = drained + 1;        // [PARTS]
+  uint8_t* cring = smem + Sh::OFF_C;
+  uint8_t* rring = smem + Sh::OFF_R;
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + Sh::OFF_BAR);  // [CST] a key tile has landed
+  uint64_t* cempty = kfull + CST;        // [CST] its block columns are done with
+  uint64_t* rempty = cempty + CST;       // [RST] its RoPE columns are
+  uint64_t* qfull = rempty + RST;        // [NQ]
+  uint64_t* qempty = qfull + NQ;         // [NQ]
+  // (two row tiles: index q; one: the score buffer, alternating)
+  uint64_t* sfull = qempty + NQ;         // [2] scores are there
+  uint64_t* sfree = sfull + 2;           // [2] and have been read into registers
+  uint64_t* pfull = sfree + 2;           // [NQ] P is there
+  uint64_t* pvdone = pfull + NQ;         // [NQ] P has been read, O is up to date
+  uint64_t* ofree = pvdone + NQ;         // [NQ] a part's O has been read
+  // (one a ring place: scores run ahead of values, so several tiles may wait for their patch)
+  uint64_t* patch = ofree + NQ;          // [CST] a key tile is ready to be patched
+  uint64_t* patched = patch + CST;       // [CST] and has been
+  uint64_t* drained = patched + CST;     // [2]
+  uint64_t* pready = drained + 2;        // [PARTS]
   uint64_t* pread = pready + Sh::PARTS;  // [PARTS]
   int4* parts = reinterpret_cast<int4*>(smem + Sh::OFF_PARTS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(parts + 3 * Sh::PARTS);
@@ -194,24 +229,25 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
 
   const int warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < CST; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
+      mbar_init(&cempty[s], 1);
+      mbar_init(&patch[s], 1);
+      mbar_init(&patched[s], 1);
     }
-    mbar_init(qfull, 1);
-    mbar_init(qempty, 1);
-    for (int s = 0; s < NQ * SB; ++s) {
-      mbar_init(&sfull[s], 1);
-      mbar_init(&pfull[s], 4);
+    for (int s = 0; s < RST; ++s) mbar_init(&rempty[s], 1);
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&sfull[q], 1);
+      mbar_init(&sfree[q], 4);
+      mbar_init(&drained[q], 1);
     }
     for (int q = 0; q < NQ; ++q) {
-      mbar_init(&ofull[q], 1);
+      mbar_init(&qfull[q], 1);
+      mbar_init(&qempty[q], 1);
+      mbar_init(&pfull[q], 4);
+      mbar_init(&pvdone[q], 1);
       mbar_init(&ofree[q], 4);
     }
-    mbar_init(pvdone, 1);
-    mbar_init(patch, 1);
-    mbar_init(patched_bar, 1);
-    mbar_init(drained, 1);
     for (int i = 0; i < Sh::PARTS; ++i) {
       mbar_init(&pready[i], 1);
       mbar_init(&pread[i], Sh::READERS);
@@ -229,7 +265,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
   // The plan, the packed query and the cleared status word come from kernels before this one. The
   // tensor memory is taken after them too, so no CTA that waits holds what an earlier one needs.
   grid_dependency_wait();
-  if (warp == Sh::MMA_WARP) {
+  if (warp == Sh::QK_WARP) {
     tmem_alloc(tmem_slot, Sh::TMEM_COLS);
     tmem_relinquish();
   }
@@ -239,15 +275,16 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
   const uint32_t tbase = *tmem_slot;
   grid_launch_dependents();
 
-  uint32_t kt = 0;    // key tiles so far (stage ring)
+  uint32_t kt = 0;    // key tiles so far (rings)
   uint32_t uc = 0;    // unit parts so far
-  uint32_t fc = 0;    // key tiles that were patched so far
+  uint32_t fixes = 0; // parity of the patches so far, a bit a ring place
   auto wait = [&](uint64_t* b, uint32_t par) {
     return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, p.wait_limit_ns));
   };
   // the next unit part from the walk warp's ring; false after the last one
   auto take = [&](UnitPart& u) {
     const int e = uc % Sh::PARTS;
+    u.valid = false;
     if (!wait(&pready[e], (uc / Sh::PARTS) & 1)) return false;
     const int4 a = parts[3 * e], b = parts[3 * e + 1];
     u.valid = parts[3 * e + 2].x != 0;
@@ -258,230 +295,257 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
     ++uc;
     return u.valid;
   };
+  // row tiles a unit part uses
+  auto rows_of = [&](const UnitPart& x) { return NQ == 2 && x.t.ntok > p.tok_tile ? 2 : 1; };
   UnitPart u;
-
   // (the register split sits in the two branches, so that each is compiled for its own share)
   if (warp >= 4 * NQ) {
-  if constexpr (Sh::REGS) regs_down<88>();
-  if (warp == Sh::LOAD_WARP) {
-    // ------------------------------ TMA loads ------------------------------
-    const uint64_t pol = l2_policy_evict_last();
-    uint32_t issued = 0, parity = 0;
-    int q_parity = -1;  // of the last query load
-    bool ok = true;
-    while (ok && take(u)) {
-      const int sub = u.sub / Sh::HALVES;
-      const int blk = sub / p.chunks;
-      const int nrow = u.t.ntok > p.tok_tile ? NQ : 1;  // row tiles in use
-      if (lane == 0) {
-        ok = mbar_wait(qempty, uc & 1, abort_flag, p.wait_limit_ns);
-        if (ok) {
-          const int rows = p.heads_tile * p.tok_tile;
-          mbar_arrive_expect_tx(qfull, nrow * rows * (Sh::DB + Sh::DR) * 2);
-          q_parity = (uc - 1) & 1;
-          for (int q = 0; q < nrow; ++q) {
-            uint8_t* dst = qbuf + q * Sh::Q_BYTES;
-            const int tok = u.t.tok0 + q * p.tok_tile;
-            for (int r = 0; r < Sh::NC; ++r)
-              tma_load_4d(dst + r * Sh::QC_REG, &map_qc, qfull, r * Sh::CW, 0, sub, tok, pol);
-            for (int r = 0; r < Sh::NR; ++r)
-              tma_load_4d(dst + Sh::NC * Sh::QC_REG + r * Sh::QR_REG, &map_qr, qfull, Sh::DB + r * Sh::RW, 0, sub,
-                          tok, pol);
+    if constexpr (Sh::REGS) regs_down<88>();
+    if (warp == Sh::LOAD_WARP) {
+      // ------------------------------ TMA loads ------------------------------
+      const uint64_t pol = l2_policy_evict_last();
+      uint32_t issued = 0, parity = 0;     // key tiles' full barriers
+      uint32_t q_issued = 0, q_parity = 0; // query barriers
+      uint32_t qc[NQ];                     // query loads so far, a row tile
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) qc[q] = 0;
+      bool ok = true;
+      while (ok && take(u)) {
+        const int sub = u.sub / Sh::HALVES;
+        const int blk = sub / p.chunks;
+        const int nrow = rows_of(u);
+        const int pages = (tile_limit(u.t, p.causal) + kPage - 1) / kPage;
+        const size_t row = (size_t)u.t.b * p.pt_stride;
+        constexpr int PPT = KT / kPage;  // pages a key tile
+        int wb = u.begin * PPT;
+        // page ids come through a window of two registers a lane, the next 32 read ahead
+        auto ids = [&](int base) {
+          const int pg = base + lane;
+          if (pg >= pages) return 0;
+          return p.page_table != nullptr ? __ldg(p.page_table + row + pg) : (int)row + pg;
+        };
+        int w0 = ids(wb), w1 = ids(wb + 32);
+        for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
+          const int p0 = t * PPT;
+          if (p0 >= wb + 32) {
+            wb += 32;
+            w0 = w1;
+            w1 = ids(wb + 32);
           }
+          int id[PPT];
+#pragma unroll
+          for (int x = 0; x < PPT; ++x) id[x] = __shfl_sync(0xffffffffu, w0, (p0 + x - wb) & 31);
+          const int npg = min(PPT, pages - p0);
+          if (lane == 0) {
+            const int s = kt % CST, rs = kt % RST;
+            const uint32_t ph = (kt / CST) & 1;
+            ok = mbar_wait(&cempty[s], ph ^ 1, abort_flag, p.wait_limit_ns) &&
+                 mbar_wait(&rempty[rs], ((kt / RST) & 1) ^ 1, abort_flag, p.wait_limit_ns);
+            if (ok) {
+              mbar_arrive_expect_tx(&kfull[s], npg * Sh::PAGE_TX);
+              issued |= 1u << s;
+              parity = (parity & ~(1u << s)) | (ph << s);
+#pragma unroll
+              for (int x = 0; x < PPT; ++x) {
+                if (x >= npg) break;
+                if (id[x] < 0 || id[x] >= p.num_pages) {
+                  set_status(p.status, kErrPageOob);
+                  id[x] = 0;
+                }
+                const int y = id[x] * kPage;
+                for (int r = 0; r < Sh::NC; ++r)
+                  tma_load_2d(cring + s * Sh::C_BYTES + r * Sh::KC_REG + x * kPage * Sh::C_ROWB, &map_c, &kfull[s],
+                              blk * Sh::DB + r * Sh::CW, y, pol);
+                for (int r = 0; r < Sh::NR; ++r)
+                  tma_load_2d(rring + rs * Sh::R_BYTES + r * Sh::KR_REG + x * kPage * Sh::R_ROWB, &map_r, &kfull[s],
+                              p.d_c + r * Sh::RW, y, pol);
+              }
+            }
+            // the part's queries, behind its first key tile (whose place is free earlier)
+            if (t == u.begin) {
+              const int rows = p.heads_tile * p.tok_tile;
+              for (int q = 0; q < nrow && ok; ++q) {
+                ok = mbar_wait(&qempty[q], (qc[q] & 1) ^ 1, abort_flag, p.wait_limit_ns);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&qfull[q], rows * (Sh::DB + Sh::DR) * 2);
+                q_issued |= 1u << q;
+                q_parity = (q_parity & ~(1u << q)) | ((qc[q] & 1) << q);
+                ++qc[q];
+                uint8_t* dst = qbuf + q * Sh::Q_BYTES;
+                const int tok = u.t.tok0 + q * p.tok_tile;
+                for (int r = 0; r < Sh::NC; ++r)
+                  tma_load_4d(dst + r * Sh::QC_REG, &map_qc, &qfull[q], r * Sh::CW, 0, sub, tok, pol);
+                for (int r = 0; r < Sh::NR; ++r)
+                  tma_load_4d(dst + Sh::NC * Sh::QC_REG + r * Sh::QR_REG, &map_qr, &qfull[q], Sh::DB + r * Sh::RW, 0,
+                              sub, tok, pol);
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      const int pages = (tile_limit(u.t, p.causal) + kPage - 1) / kPage;
-      const size_t row = (size_t)u.t.b * p.pt_stride;
-      constexpr int PPT = KT / kPage;  // pages a key tile
-      int wb = u.begin * PPT;
-      // page ids come through a window of two registers a lane, the next 32 read ahead
-      auto ids = [&](int base) {
-        const int pg = base + lane;
-        if (pg >= pages) return 0;
-        return p.page_table != nullptr ? __ldg(p.page_table + row + pg) : (int)row + pg;
-      };
-      int w0 = ids(wb), w1 = ids(wb + 32);
-      for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
-        const int p0 = t * PPT;
-        if (p0 >= wb + 32) {
-          wb += 32;
-          w0 = w1;
-          w1 = ids(wb + 32);
-        }
-        int id[PPT];
+      if (lane == 0) {
+        // nothing may still be landing when the CTA's shared memory is released
+        for (int s = 0; s < CST; ++s)
+          if ((issued >> s) & 1)
+            if (!mbar_wait_drain(&kfull[s], (parity >> s) & 1, p.wait_limit_ns)) *drain_err = 1;
+        for (int q = 0; q < NQ; ++q)
+          if ((q_issued >> q) & 1)
+            if (!mbar_wait_drain(&qfull[q], (q_parity >> q) & 1, p.wait_limit_ns)) *drain_err = 1;
+      }
+    } else if (warp == Sh::QK_WARP) {
+      // ------------------------------ scores ------------------------------
+      const bool one = elect_lane();
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, KT, false, false);
+      constexpr uint32_t c_hi = desc_hi(8 * Sh::C_ROWB, swizzle_code(Sh::C_ROWB));
+      constexpr uint32_t r_hi = desc_hi(8 * Sh::R_ROWB, swizzle_code(Sh::R_ROWB));
+      const uint32_t q_lo = desc_lo(smem_u32(qbuf), 16), c_lo = desc_lo(smem_u32(cring), 16);
+      const uint32_t r_lo = desc_lo(smem_u32(rring), 16);
+      uint32_t sc[NQ], qc[NQ];  // score tiles and queries so far
 #pragma unroll
-        for (int x = 0; x < PPT; ++x) id[x] = __shfl_sync(0xffffffffu, w0, (p0 + x - wb) & 31);
-        const int npg = min(PPT, pages - p0);
-        if (lane == 0) {
-          const int s = kt % STAGES;
-          const uint32_t ph = (kt / STAGES) & 1;
-          ok = mbar_wait(&kempty[s], ph ^ 1, abort_flag, p.wait_limit_ns);
-          if (ok) {
-            uint8_t* dst = stages + s * Sh::STAGE_BYTES;
-            mbar_arrive_expect_tx(&kfull[s], npg * Sh::PAGE_TX);
-            issued |= 1u << s;
-            parity = (parity & ~(1u << s)) | (ph << s);
+      for (int q = 0; q < NQ; ++q) sc[q] = qc[q] = 0;
+      int last = -1;            // two row tiles: whose scores the buffer holds
+      bool ok = true;
+      while (ok && take(u)) {
+        const int n = u.end - u.begin, nrow = rows_of(u);
+        for (int i = 0; i < n && ok; ++i, ++kt) {
+          ok = wait(&kfull[kt % CST], (kt / CST) & 1);
 #pragma unroll
-            for (int x = 0; x < PPT; ++x) {
-              if (x >= npg) break;
-              if (id[x] < 0 || id[x] >= p.num_pages) {
-                set_status(p.status, kErrPageOob);
-                id[x] = 0;
-              }
-              const int y = id[x] * kPage;
+          for (int q = 0; q < NQ; ++q) {
+            if (q >= nrow || !ok) break;
+            if (i == 0) {
+              ok = wait(&qfull[q], qc[q] & 1);
+              ++qc[q];
+            }
+            // the score buffer's last contents are in registers
+            if (NQ == 1) {
+              if (kt >= 2) ok = ok && wait(&sfree[kt & 1], ((kt >> 1) - 1) & 1);
+            } else if (last >= 0) {
+              ok = ok && (last == 0 ? wait(&sfree[0], (sc[0] - 1) & 1) : wait(&sfree[1], (sc[NQ - 1] - 1) & 1));
+            }
+            if (!ok) break;
+            last = q;
+            ++sc[q];
+            tc_fence_after();
+            const uint32_t a0 = q_lo + q * (Sh::Q_BYTES >> 4), b0 = c_lo + (kt % CST) * (Sh::C_BYTES >> 4);
+            const uint32_t b1 = r_lo + (kt % RST) * (Sh::R_BYTES >> 4);
+            const uint32_t d = tbase + Sh::S_COL + (NQ == 1 ? (kt & 1) * KT : 0);
+            if (one) {
+#pragma unroll
               for (int r = 0; r < Sh::NC; ++r)
-                tma_load_2d(dst + r * Sh::KC_REG + x * kPage * Sh::C_ROWB, &map_c, &kfull[s], blk * Sh::DB + r * Sh::CW,
-                            y, pol);
+#pragma unroll
+                for (int ks = 0; ks < Sh::C_ROWB / 32; ++ks)
+                  umma_ss(d, a0 + ((r * Sh::QC_REG + ks * 32) >> 4), c_hi, b0 + ((r * Sh::KC_REG + ks * 32) >> 4), c_hi,
+                          idesc_qk, (r > 0 || ks > 0) ? 1u : 0u);
+#pragma unroll
               for (int r = 0; r < Sh::NR; ++r)
-                tma_load_2d(dst + Sh::NC * Sh::KC_REG + r * Sh::KR_REG + x * kPage * Sh::R_ROWB, &map_r, &kfull[s],
-                            p.d_c + r * Sh::RW, y, pol);
+#pragma unroll
+                for (int ks = 0; ks < Sh::R_ROWB / 32; ++ks)
+                  umma_ss(d, a0 + ((Sh::NC * Sh::QC_REG + r * Sh::QR_REG + ks * 32) >> 4), r_hi,
+                          b1 + ((r * Sh::KR_REG + ks * 32) >> 4), r_hi, idesc_qk, 1u);
+              umma_commit(&sfull[NQ == 1 ? kt & 1 : q]);
+              if (i == n - 1) umma_commit(&qempty[q]);
+              if (q == nrow - 1) {
+                umma_commit(&rempty[kt % RST]);
+                // a tile that reaches past what the part's first token sees is patched (see the patch
+                // warp) between its score MMAs and its value MMAs
+                if ((u.begin + i + 1) * KT > u.t.lim0) umma_commit(&patch[kt % CST]);
+              }
             }
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-    }
-    if (lane == 0) {
-      // nothing may still be landing when the CTA's shared memory is released
-      for (int s = 0; s < STAGES; ++s)
-        if ((issued >> s) & 1)
-          if (!mbar_wait_drain(&kfull[s], (parity >> s) & 1, p.wait_limit_ns)) *drain_err = 1;
-      if (q_parity >= 0 && !mbar_wait_drain(qfull, q_parity, p.wait_limit_ns)) *drain_err = 1;
-    }
-  } else if (warp == Sh::MMA_WARP) {
-    // ------------------------------ MMAs ------------------------------
-    const bool one = elect_lane();
-    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, KT, false, false);
-    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV, false, true);
-    constexpr uint32_t c_hi = desc_hi(8 * Sh::C_ROWB, swizzle_code(Sh::C_ROWB));
-    constexpr uint32_t r_hi = desc_hi(8 * Sh::R_ROWB, swizzle_code(Sh::R_ROWB));
-    const uint32_t q_lo = desc_lo(smem_u32(qbuf), 16), k_lo = desc_lo(smem_u32(stages), 16);
-    const uint32_t v_lo = desc_lo(smem_u32(stages), Sh::KC_REG);
-    auto issue_qk = [&](int q, uint32_t tile) {
-      const uint32_t a0 = q_lo + q * (Sh::Q_BYTES >> 4), b0 = k_lo + (tile % STAGES) * (Sh::STAGE_BYTES >> 4);
-      const uint32_t sbuf = q * SB + (SB == 2 ? tile & 1 : 0);
-      const uint32_t d = tbase + Sh::S_COL + sbuf * KT;
-      if (one) {
+      if (one) umma_commit(&drained[0]);
+      if (!mbar_wait_drain(&drained[0], 0, p.wait_limit_ns)) *drain_err = 1;
+      __syncwarp();
+    } else if (warp == Sh::PV_WARP) {
+      // ------------------------------ values ------------------------------
+      const bool one = elect_lane();
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV, false, true);
+      constexpr uint32_t c_hi = desc_hi(8 * Sh::C_ROWB, swizzle_code(Sh::C_ROWB));
+      const uint32_t v_lo = desc_lo(smem_u32(cring), Sh::KC_REG);
+      uint32_t pc[NQ], oc[NQ];  // P tiles and parts so far
 #pragma unroll
-        for (int r = 0; r < Sh::NC; ++r)
+      for (int q = 0; q < NQ; ++q) pc[q] = oc[q] = 0;
+      bool ok = true;
+      while (ok && take(u)) {
+        const int n = u.end - u.begin, nrow = rows_of(u);
+        const uint32_t half = (u.sub % Sh::HALVES) * ((DV / Sh::CW) * (Sh::KC_REG >> 4));
+        for (int i = 0; i < n && ok; ++i, ++kt) {
 #pragma unroll
-          for (int ks = 0; ks < Sh::C_ROWB / 32; ++ks)
-            umma_ss(d, a0 + ((r * Sh::QC_REG + ks * 32) >> 4), c_hi, b0 + ((r * Sh::KC_REG + ks * 32) >> 4), c_hi,
-                    idesc_qk, (r > 0 || ks > 0) ? 1u : 0u);
+          for (int q = 0; q < NQ; ++q) {
+            if (q >= nrow || !ok) break;
+            ok = wait(&pfull[q], pc[q] & 1);
+            ++pc[q];
+            if (q == 0 && (u.begin + i + 1) * KT > u.t.lim0) {
+              ok = ok && wait(&patched[kt % CST], (fixes >> (kt % CST)) & 1);
+              fixes ^= 1u << (kt % CST);
+            }
+            if (i == 0) {
+              ok = ok && wait(&ofree[q], (oc[q] & 1) ^ 1);
+              ++oc[q];
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t b0 = v_lo + (kt % CST) * (Sh::C_BYTES >> 4) + half;
+            const uint32_t a = tbase + Sh::P_COL + q * (KT / 2);
+            if (one) {
 #pragma unroll
-        for (int r = 0; r < Sh::NR; ++r)
-#pragma unroll
-          for (int ks = 0; ks < Sh::R_ROWB / 32; ++ks)
-            umma_ss(d, a0 + ((Sh::NC * Sh::QC_REG + r * Sh::QR_REG + ks * 32) >> 4), r_hi,
-                    b0 + ((Sh::NC * Sh::KC_REG + r * Sh::KR_REG + ks * 32) >> 4), r_hi, idesc_qk, 1u);
-        umma_commit(&sfull[sbuf]);
+              for (int ks = 0; ks < KT / 16; ++ks)
+                umma_ts(tbase + Sh::O_COL + q * DV, a + ks * 8, b0 + ((ks * 16 * Sh::C_ROWB) >> 4), c_hi, idesc_pv,
+                        (i > 0 || ks > 0) ? 1u : 0u);
+              umma_commit(&pvdone[q]);
+              // (every score of the tile was formed before the last row tile's P)
+              if (q == nrow - 1) umma_commit(&cempty[kt % CST]);
+            }
+          }
+        }
       }
-    };
-    auto issue_pv = [&](int q, uint32_t tile, int half, bool first) {
-      const uint32_t b0 = v_lo + (tile % STAGES) * (Sh::STAGE_BYTES >> 4) + half * ((DV / Sh::CW) * (Sh::KC_REG >> 4));
-      const uint32_t sbuf = q * SB + (SB == 2 ? tile & 1 : 0);
-      const uint32_t a = tbase + Sh::S_COL + sbuf * KT;
-      if (one) {
-#pragma unroll
-        for (int ks = 0; ks < KT / 16; ++ks)
-          umma_ts(tbase + Sh::O_COL + q * DV, a + ks * 8, b0 + ((ks * 16 * Sh::C_ROWB) >> 4), c_hi, idesc_pv,
-                  (first && ks == 0) ? 0u : 1u);
-      }
-    };
-    auto commit = [&](uint64_t* b) {
-      if (one) umma_commit(b);
-    };
-    uint32_t pc[NQ];  // score tiles so far, a row tile
-    uint32_t oc[NQ];  // parts so far, a row tile
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) pc[q] = oc[q] = 0;
-    bool ok = true;
-    while (ok && take(u)) {
-      const int half = u.sub % Sh::HALVES;
-      const int nrow = NQ == 2 && u.t.ntok > p.tok_tile ? 2 : 1;
-      const int n = u.end - u.begin;
-      ok = wait(qfull, (uc - 1) & 1) && wait(&kfull[kt % STAGES], (kt / STAGES) & 1);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int q = 0; q < NQ; ++q)
-        if (q < nrow) issue_qk(q, kt);
-      // a tile that reaches past what the unit's first token sees is patched (see the patch
-      // warp) between its score MMAs and its value MMAs
-      auto patched = [&](int i) { return (u.begin + i + 1) * KT > u.t.lim0; };
-      if (patched(0)) commit(patch);
-      if (n == 1) commit(qempty);
-      // the next tile's scores go out before this tile's values where a second stage holds it
-      auto next_qk = [&](int i) {
-        if (i + 1 >= n) return true;
-        const uint32_t tile = kt + i + 1;
-        if (!wait(&kfull[tile % STAGES], (tile / STAGES) & 1)) return false;
-        tc_fence_after();
-        issue_qk(0, tile);
-        if (patched(i + 1)) commit(patch);
-        if (i + 2 == n) commit(qempty);
+      if (one) umma_commit(&drained[1]);
+      if (!mbar_wait_drain(&drained[1], 0, p.wait_limit_ns)) *drain_err = 1;
+      __syncwarp();
+    } else if (warp == Sh::FIX_WARP) {
+      // ------------------------------ patches ------------------------------
+      // A masked key has P = 0, but 0 x NaN is NaN: where a key tile reaches past what the unit's
+      // first token sees, the value rows no token of the unit sees are zeroed (they may lie past the
+      // sequence's end, where a slot may hold anything), and elements of the rows that only some of
+      // its tokens see are zeroed where they are not finite. A token that does see such a row gets
+      // its NaN through the score, whose MMA has read the tile before it is patched.
+      // This warp also walks the plan and hands the unit parts out, two ahead of the one it is at.
+      const int tiles = __ldg(p.plan.hdr);
+      UnitWalk walk;
+      walk.init(&p.plan, tiles, stretch_of(__ldg(p.plan.start + tiles), blockIdx.x, gridDim.x), p.nsub * Sh::HALVES,
+                KT, p.causal);
+      uint32_t given = 0;
+      bool more = true;
+      auto give = [&]() {
+        const UnitPart g = walk.next();
+        const int e = given % Sh::PARTS;
+        if (!wait(&pread[e], ((given / Sh::PARTS) & 1) ^ 1)) return false;
+        if (lane == 0) {
+          parts[3 * e] = make_int4(g.t.b, g.t.tok0, g.t.ntok, g.t.lim0);
+          parts[3 * e + 1] = make_int4(g.sub, g.kv, g.begin, g.end);
+          parts[3 * e + 2].x = g.valid;
+          mbar_arrive(&pready[e]);
+        }
+        __syncwarp();
+        ++given;
+        more = g.valid;
         return true;
       };
-      for (int i = 0; i < n && ok; ++i) {
-        const uint32_t tile = kt + i;
-        if (NQ == 1 && STAGES > 1) ok = next_qk(i);
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if (q >= nrow || !ok) break;
-          const uint32_t pb = q * SB + (SB == 2 ? tile & 1 : 0);
-          const uint32_t pph = SB == 2 ? (tile >> 1) & 1 : pc[q] & 1;
-          ok = wait(&pfull[pb], pph);
-          if (ok && q == 0 && patched(i)) ok = wait(patched_bar, fc & 1);
-          if (ok && i == 0) ok = wait(&ofree[q], (oc[q] & 1) ^ 1);
-          if (!ok) break;
-          ++pc[q];
-          tc_fence_after();
-          issue_pv(q, tile, half, i == 0);
-          if (q == nrow - 1) commit(&kempty[tile % STAGES]);
-          if (NQ == 1) commit(pvdone);
-          if (i == n - 1) {
-            commit(&ofull[q]);
-            ++oc[q];
-          }
-          if (NQ == 2 && i + 1 < n) {
-            if (q == 0) {
-              ok = wait(&kfull[(tile + 1) % STAGES], ((tile + 1) / STAGES) & 1);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            issue_qk(q, tile + 1);
-            if (q == nrow - 1) {
-              if (patched(i + 1)) commit(patch);
-              if (i + 2 == n) commit(qempty);
-            }
-          }
-        }
-        if (patched(i)) ++fc;
-        if (NQ == 1 && STAGES == 1 && ok) ok = next_qk(i);
-      }
-      kt += n;
-    }
-    commit(drained);
-    if (!mbar_wait_drain(drained, 0, p.wait_limit_ns)) *drain_err = 1;
-    __syncwarp();
-  } else if (warp == Sh::FIX_WARP) {
-    // ------------------------------ patches ------------------------------
-    // A masked key has P = 0, but 0 x NaN is NaN: where a key tile reaches past what the unit's
-    // first token sees, the value rows no token of the unit sees are zeroed (they may lie past the
-    // sequence's end, where a slot may hold anything), and elements of the rows that only some of
-    // its tokens see are zeroed where they are not finite. A token that does see such a row gets
-    // its NaN through the score, whose MMA has read the tile before it is patched.
-    bool ok = true;
-    while (ok && take(u)) {
-      const int lim = tile_limit(u.t, p.causal);
-      for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
-        if ((t + 1) * KT > u.t.lim0) {
+      bool ok = give();
+      if (ok && more) ok = give();
+      while (ok && take(u)) {
+        if (more) ok = give();
+        if (!ok) break;
+        const int lim = tile_limit(u.t, p.causal);
+        for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
+          if ((t + 1) * KT <= u.t.lim0) continue;
           // the MMAs that form this key tile's scores have read it (and it had landed)
-          ok = wait(patch, fc & 1) && wait(&kfull[kt % STAGES], (kt / STAGES) & 1);
+          ok = wait(&patch[kt % CST], (fixes >> (kt % CST)) & 1) && wait(&kfull[kt % CST], (kt / CST) & 1);
           if (!ok) break;
-          ++fc;
-          uint8_t* st_mem = stages + (kt % STAGES) * Sh::STAGE_BYTES;
+          fixes ^= 1u << (kt % CST);
+          uint8_t* st_mem = cring + (kt % CST) * Sh::C_BYTES;
           const int k0 = t * KT;
           const int some = max(0, min(KT, max(u.t.lim0, 0) - k0));  // rows [some, none) only some tokens see
           const int none = max(0, min(KT, lim - k0));
@@ -491,43 +555,23 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
             for (int i = none * CPR + lane; i < KT * CPR; i += 32)
               *reinterpret_cast<uint4*>(reg + i * 16) = make_uint4(0, 0, 0, 0);
             for (int i = some * CPR + lane; i < none * CPR; i += 32) {
-              uint4 v = *reinterpret_cast<const uint4*>(reg + i * 16);
-              uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+              uint4 x = *reinterpret_cast<const uint4*>(reg + i * 16);
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
               bool hit = false;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; hit = true; }
                 if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0x0000ffffu; hit = true; }
               }
-              if (hit) *reinterpret_cast<uint4*>(reg + i * 16) = v;
+              if (hit) *reinterpret_cast<uint4*>(reg + i * 16) = x;
             }
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(patched_bar);
+          if (lane == 0) mbar_arrive(&patched[kt % CST]);
         }
       }
     }
-  } else if (warp == Sh::WALK_WARP) {
-    // ------------------------------ the walk ------------------------------
-    const int tiles = __ldg(p.plan.hdr);
-    UnitWalk walk;
-    walk.init(&p.plan, tiles, stretch_of(__ldg(p.plan.start + tiles), blockIdx.x, gridDim.x), p.nsub * Sh::HALVES, KT,
-              p.causal);
-    do {
-      u = walk.next();
-      const int e = uc % Sh::PARTS;
-      if (!wait(&pread[e], ((uc / Sh::PARTS) & 1) ^ 1)) break;
-      if (lane == 0) {
-        parts[3 * e] = make_int4(u.t.b, u.t.tok0, u.t.ntok, u.t.lim0);
-        parts[3 * e + 1] = make_int4(u.sub, u.kv, u.begin, u.end);
-        parts[3 * e + 2].x = u.valid;
-        mbar_arrive(&pready[e]);
-      }
-      __syncwarp();
-      ++uc;
-    } while (u.valid);
-  }
   } else {
     if constexpr (Sh::REGS) regs_up<208>();
     // ------------------------------ softmax and results ------------------------------
@@ -540,27 +584,27 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
     const int hr = row - tl * p.heads_tile;                // head within the tile's heads
     const int tok = q * p.tok_tile + tl;                   // token within the unit
     const bool row_in = tl < p.tok_tile;
-    uint32_t sc = 0, oc = 0;
+    const uint32_t o_addr = tbase + lane_base + Sh::O_COL + q * DV;
+    uint32_t sc = 0;                                       // score tiles so far
     bool ok = true;
     const float sc_mul = p.s_scale, slack = 8.f / sc_mul;
     while (ok && take(u)) {
       const int n = u.end - u.begin;
-      if (q > 0 && u.t.ntok <= p.tok_tile) {
-        kt += n;
-        continue;
-      }
+      if (q >= rows_of(u)) continue;
       const int lim = p.causal ? u.t.lim0 + tok : u.t.lim0;  // keys this row sees
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < n; ++i, ++kt, ++sc) {
-        const uint32_t sb = q * SB + (SB == 2 ? kt & 1 : 0);
-        const uint32_t par = SB == 2 ? (kt >> 1) & 1 : sc & 1;
-        ok = wait(&sfull[sb], par);
+      for (int i = 0; i < n; ++i, ++sc) {
+        ok = NQ == 1 ? wait(&sfull[sc & 1], (sc >> 1) & 1) : wait(&sfull[q], sc & 1);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t s_addr = tbase + lane_base + Sh::S_COL + sb * KT;
+        const uint32_t s_addr = tbase + lane_base + Sh::S_COL + (NQ == 1 ? (sc & 1) * KT : 0);
+        const uint32_t p_addr = tbase + lane_base + Sh::P_COL + q * (KT / 2);
         float s[KT];
         tmem_load_row<KT>(s_addr, s);
         tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfree[NQ == 1 ? sc & 1 : q]);
         const int k0 = (u.begin + i) * KT;
         if (k0 + KT > u.t.lim0) {
 #pragma unroll
@@ -577,16 +621,14 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         x0 = max3_nan(x0, s[KT - 4], s[KT - 3]);
         x1 = max3_nan(x1, s[KT - 2], s[KT - 1]);
         const float mt = max3_nan(max3_nan(x0, x1, x2), x3, x3);
+        // P's place is free and O holds the sums up to the tile before
+        if (sc > 0) ok = wait(&pvdone[q], (sc - 1) & 1);
+        if (!ok) break;
         if (i == 0) {
           m = mt;
         } else {
           const bool raise = mt > m + slack;
           if (__any_sync(0xffffffffu, raise)) {
-            // with one score buffer this tile's scores were issued after the last PV; with two the
-            // last PV has its own barrier
-            // (waited for from the phase before it, so that the parity is that phase's)
-            if (NQ == 1) ok = (kt < 2 || wait(pvdone, kt & 1)) && wait(pvdone, (kt - 1) & 1);
-            if (!ok) break;
             tc_fence_after();
             const float a = raise ? fast_exp2((m - mt) * sc_mul) : 1.f;
             l *= a;
@@ -594,11 +636,11 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
 #pragma unroll 1
             for (int c = 0; c < DV; c += 32) {
               float o[32];
-              tmem_load_row<32>(tbase + lane_base + Sh::O_COL + q * DV + c, o);
+              tmem_load_row<32>(o_addr + c, o);
               tmem_ld_wait();
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] *= a;
-              tmem_store_row<32>(tbase + lane_base + Sh::O_COL + q * DV + c, o);
+              tmem_store_row<32>(o_addr + c, o);
             }
             tmem_st_wait();
           }
@@ -618,49 +660,60 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
             else add_f32x2(l0, l1, l0, l1, e0, e1);
             pk[c / 2] = pack_bf16x2(e0, e1);  // P to bf16 (half a step 2^-8 relative) for the tensor core
           }
-          tmem_st32(s_addr + c0 / 2, pk);
+          tmem_st32(p_addr + c0 / 2, pk);
         }
         l += (l0 + l1) + (l2 + l3);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[sb]);
+        if (lane == 0) mbar_arrive(&pfull[q]);
       }
       if (!ok) break;
-      ok = wait(&ofull[q], oc & 1);
+      ok = wait(&pvdone[q], (sc - 1) & 1);
       if (!ok) break;
-      ++oc;
       tc_fence_after();
       // ---- results of this part ----
       const int half = u.sub % Sh::HALVES, sub = u.sub / Sh::HALVES;
-      const int head = (sub / p.chunks) * p.heads_block + (sub % p.chunks) * p.heads_tile + hr;
+      const int head0 = (sub / p.chunks) * p.heads_block + (sub % p.chunks) * p.heads_tile;
       const bool mine = row_in && tok < u.t.ntok;
       const bool whole = u.begin == 0 && u.end == u.kv;
       const int slot = 2 * blockIdx.x + (u.begin == 0 ? 1 : 0);
       const float inv = l > 0.f ? p.o_scale / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
       const float lse2 = l == 0.f ? -INFINITY : m * sc_mul + __log2f(l);
-      const size_t at = (size_t)(u.t.tok0 + tok) * p.vh + head;
+      const size_t at = (size_t)(u.t.tok0 + tok) * p.vh + head0 + hr;
       const size_t pat = (size_t)slot * Sh::ROWS + q * 128 + row;
-      if (mine && half == 0) {
+      if (mine) {
         if (!whole)
           p.part_lse[pat] = lse2;
-        else if (p.lse != nullptr)
+        else if (half == 0 && p.lse != nullptr)
           p.lse[at] = p.o_bf16 != nullptr ? lse2 * kLn2 : lse2;
       }
-      if (mine && half != 0 && !whole) p.part_lse[pat] = lse2;
+      // where this lane's four rows (see exchange4) go, or null
+      __nv_bfloat16* dst4[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int rr = (row & ~3) + r, t4 = rr / p.heads_tile, tk = q * p.tok_tile + t4;
+        const bool in = t4 < p.tok_tile && tk < u.t.ntok && whole && p.o_bf16 != nullptr;
+        const size_t a4 = (size_t)(u.t.tok0 + tk) * p.vh + head0 + (rr - t4 * p.heads_tile);
+        dst4[r] = in ? p.o_bf16 + a4 * Sh::DB + half * DV + (lane & 3) * 8 : nullptr;
+      }
 #pragma unroll 1
       for (int c = 0; c < DV; c += 32) {
         float o[32];
-        tmem_load_row<32>(tbase + lane_base + Sh::O_COL + q * DV + c, o);
+        tmem_load_row<32>(o_addr + c, o);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] *= inv;
-        if (mine && whole && p.o_bf16 != nullptr) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o_bf16 + at * Sh::DB + half * DV + c);
+        if (whole && p.o_bf16 != nullptr) {
+          uint4 v4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+            v4[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                               pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+          exchange4(v4, lane);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (dst4[r] != nullptr) *reinterpret_cast<uint4*>(dst4[r] + c) = v4[r];
         } else if (mine) {
           float4* dst = reinterpret_cast<float4*>(whole ? p.o_f32 + at * Sh::DB + half * DV + c : p.part_o + pat * DV + c);
 #pragma unroll
@@ -680,7 +733,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
     if (*abort_flag) set_status(p.status, kErrTimeout);
     if (*drain_err) force_status(p.status, kErrDrain);
   }
-  if (warp == Sh::MMA_WARP) {
+  if (warp == Sh::QK_WARP) {
     tc_fence_after();
     tmem_dealloc(tbase, Sh::TMEM_COLS);
   }

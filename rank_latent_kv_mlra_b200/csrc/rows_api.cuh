@@ -8,10 +8,10 @@ namespace {
 // turn; at d_b = 256 a row tile's O fills half the tensor memory, so one row tile alternates two
 // score buffers over 64-key tiles; at d_b = 512 two CTAs keep a half of O each and both form the
 // scores (64 % of their MMA work is then O(1) repeated, but no exchange between SMs is needed).
-using RowsTiny = RowShape<32, 16, 128, 32, 2, 4>;
-using RowsB128 = RowShape<128, 64, 128, 128, 2, 2>;
-using RowsB256 = RowShape<256, 64, 64, 256, 1, 3>;
-using RowsB512 = RowShape<512, 64, 64, 256, 1, 1>;
+using RowsTiny = RowShape<32, 16, 128, 32, 2, 4, 4>;
+using RowsB128 = RowShape<128, 64, 128, 128, 2, 3, 2>;
+using RowsB256 = RowShape<256, 64, 64, 256, 1, 3, 3>;
+using RowsB512 = RowShape<512, 64, 64, 256, 1, 1, 1>;
 
 constexpr int kMaxQueryTokens = 1 << 21;  // grid rows of the absorb kernel
 
