@@ -45,25 +45,30 @@ __device__ __forceinline__ int unit_cost(int kv) { return kv > 0 ? kv + kUnitCos
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxSeqs = 4096;
 
+// Exclusive scan over the block's threads (32 warps at most); scratch holds a value a warp. Every
+// thread must have read the last call's result before the next call writes scratch: the first
+// barrier sees to that.
 template <class T>
-__device__ __forceinline__ T block_exclusive_scan(T v, T* scratch, T* total) {
-  T x = v;
+__device__ __forceinline__ T warp_inclusive_scan(T x) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane_id() >= o) x += y;
   }
+  return x;
+}
+template <class T>
+__device__ __forceinline__ T block_exclusive_scan(T v, T* scratch, T* total) {
+  const T x = warp_inclusive_scan(v);
   __syncthreads();
   if (lane_id() == 31) scratch[warp_id()] = x;
   __syncthreads();
-  T before = 0, all = 0;
+  // every warp scans the warps' sums
   const int nw = blockDim.x >> 5;
-  for (int w = 0; w < nw; ++w) {
-    if (w < warp_id()) before += scratch[w];
-    all += scratch[w];
-  }
-  *total = all;
-  return before + x - v;
+  const T s = warp_inclusive_scan(lane_id() < nw ? scratch[lane_id()] : T(0));
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  const T before = __shfl_sync(0xffffffffu, s, max(warp_id() - 1, 0));
+  return (warp_id() > 0 ? before : T(0)) + x - v;
 }
 
 // One CTA. Bounded by latency: a block scan per 1024 token tiles.

@@ -585,6 +585,14 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
     const int tok = q * p.tok_tile + tl;                   // token within the unit
     const bool row_in = tl < p.tok_tile;
     const uint32_t o_addr = tbase + lane_base + Sh::O_COL + q * DV;
+    // the four rows this lane stores a piece of (see exchange4): their tokens and places in a part
+    int tok4[4], off4[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int rr = (row & ~3) + r, t4 = rr / p.heads_tile;
+      tok4[r] = t4 < p.tok_tile ? q * p.tok_tile + t4 : 0x7fffffff;
+      off4[r] = ((q * p.tok_tile + t4) * p.vh + (rr - t4 * p.heads_tile)) * Sh::DB + (lane & 3) * 8;
+    }
     uint32_t sc = 0;                                       // score tiles so far
     bool ok = true;
     const float sc_mul = p.s_scale, slack = 8.f / sc_mul;
@@ -607,8 +615,14 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         if (lane == 0) mbar_arrive(&sfree[NQ == 1 ? sc & 1 : q]);
         const int k0 = (u.begin + i) * KT;
         if (k0 + KT > u.t.lim0) {
+          // 16 keys at a time: those every row of the warp sees are left alone
+          const int seen = lim - k0;
 #pragma unroll
-          for (int c = 0; c < KT; ++c) s[c] = k0 + c < lim ? s[c] : -INFINITY;
+          for (int c0 = 0; c0 < KT; c0 += 16) {
+            if (__all_sync(0xffffffffu, seen >= c0 + 16)) continue;
+#pragma unroll
+            for (int c = c0; c < c0 + 16; ++c) s[c] = c < seen ? s[c] : -INFINITY;
+          }
         }
         float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
 #pragma unroll
@@ -688,15 +702,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         else if (half == 0 && p.lse != nullptr)
           p.lse[at] = p.o_bf16 != nullptr ? lse2 * kLn2 : lse2;
       }
-      // where this lane's four rows (see exchange4) go, or null
-      __nv_bfloat16* dst4[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int rr = (row & ~3) + r, t4 = rr / p.heads_tile, tk = q * p.tok_tile + t4;
-        const bool in = t4 < p.tok_tile && tk < u.t.ntok && whole && p.o_bf16 != nullptr;
-        const size_t a4 = (size_t)(u.t.tok0 + tk) * p.vh + head0 + (rr - t4 * p.heads_tile);
-        dst4[r] = in ? p.o_bf16 + a4 * Sh::DB + half * DV + (lane & 3) * 8 : nullptr;
-      }
+      __nv_bfloat16* const out = p.o_bf16 + ((size_t)u.t.tok0 * p.vh + head0) * Sh::DB + half * DV;
 #pragma unroll 1
       for (int c = 0; c < DV; c += 32) {
         float o[32];
@@ -713,7 +719,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
           exchange4(v4, lane);
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (dst4[r] != nullptr) *reinterpret_cast<uint4*>(dst4[r] + c) = v4[r];
+            if (tok4[r] < u.t.ntok) *reinterpret_cast<uint4*>(out + off4[r] + c) = v4[r];
         } else if (mine) {
           float4* dst = reinterpret_cast<float4*>(whole ? p.o_f32 + at * Sh::DB + half * DV + c : p.part_o + pat * DV + c);
 #pragma unroll
@@ -1007,19 +1013,25 @@ __global__ void __launch_bounds__(Sh::THREADS)
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] *= p.out_scale;
-        const size_t at = ((size_t)tok * p.heads + h) * DH + c;
-        if (tok >= used) {
-          // rows behind the last sequence stay as they were
-        } else if (p.out_f32) {
-          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+        // rows behind the last sequence (tok >= used) stay as they were
+        if (p.out_f32) {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((size_t)tok * p.heads + h) * DH + c);
+          if (tok < used) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at);
+          uint4 v4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
-                                pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+            v4[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                               pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+          exchange4(v4, lane);
+          const int t0 = tok - (lane & 3);
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((size_t)t0 * p.heads + h) * DH + c + (lane & 3) * 8;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (t0 + r < used) *reinterpret_cast<uint4*>(dst + (size_t)r * p.heads * DH) = v4[r];
         }
         __syncwarp();
       }

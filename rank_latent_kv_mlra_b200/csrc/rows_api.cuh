@@ -268,7 +268,7 @@ cudaError_t launch_merge(const mlra_ctx* h, const RowsCall& c, cudaStream_t s) {
     m.o_bf16 = c.rp.o_bf16;
     m.lse = c.rp.lse;
     cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = launch_cfg(dim3(h->num_sms, 8), dim3(256), 0, s, true, &attr);
+    cudaLaunchConfig_t cfg = launch_cfg(dim3(h->num_sms, Sh::ROWS / 8), dim3(256), 0, s, true, &attr);
     return cudaLaunchKernelEx(&cfg, mlra_rows_merge_kernel, m);
   });
 }
