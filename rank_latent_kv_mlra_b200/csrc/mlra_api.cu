@@ -752,7 +752,7 @@ int mlra_decode_latent(mlra_handle h, const void* q, mlra_dtype q_dtype, const v
 
 int mlra_prefill_workspace_size(mlra_handle h, int total_q, int batch, int pt_stride, size_t* bytes) {
   if (!h || !bytes || !rows_sizes_ok(total_q, batch, pt_stride)) return MLRA_ERR_INVALID_ARG;
-  *bytes = carve_prefill(h, total_q, batch, pt_stride, nullptr).bytes;
+  *bytes = prefill_bytes(h, total_q, batch, pt_stride);
   return MLRA_OK;
 }
 

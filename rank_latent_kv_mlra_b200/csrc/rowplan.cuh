@@ -18,10 +18,13 @@ struct TokenTile {
   int b, tok0, ntok, lim0;
 };
 struct RowPlan {
-  int* hdr;            // [0] token tiles, [1] tokens in use (cu[batch]), [2] bad lengths found
+  int* hdr;            // [0] token tiles, [1] tokens in use (cu[batch]), [2] bad lengths found,
+                       // [3] token tiles without a key
   long long* start;    // [max tiles + 1] position of each tile's first unit; the last is the total
   TokenTile* tile;     // [max tiles]
   int* tok_tile;       // [tokens] tile of each token, or null
+  int4* cut;           // [2 * CTAs] the unit each CTA's stretch goes on with: first and last CTA, unit;
+                       // first token, tokens (written by the attention kernel, for the merge)
 };
 struct RowPlanParams {
   const int* cu;       // [batch + 1] first query token of each sequence
@@ -76,7 +79,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const R
   __shared__ int base[kMaxSeqs + 1];  // first token tile of each sequence
   __shared__ long long scratch[32];
   __shared__ int scratch_i[32];
-  __shared__ int flags[2];
+  __shared__ int flags[2];  // bad lengths; tiles without a key
   if (threadIdx.x < 2) flags[threadIdx.x] = 0;
   __syncthreads();
   grid_launch_dependents();
@@ -127,6 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const R
       t.ntok = min(p.tile_tokens, n_q - first);
       t.lim0 = p.causal ? len - n_q + first + 1 : len;
       cost = (long long)unit_cost(key_tiles(t, p.causal, p.key_tile)) * p.units;
+      if (cost == 0) atomicAdd(&flags[1], 1);
     }
     long long all;
     const long long at = pos + block_exclusive_scan<long long>(cost, scratch, &all);
@@ -138,7 +142,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const R
     }
     pos += all;
   }
+  __syncthreads();
   if (threadIdx.x == 0) {
+    p.plan.hdr[3] = flags[1];
     p.plan.start[tiles] = pos;
     p.plan.hdr[0] = tiles;
     p.plan.hdr[1] = (flags[0] & 2) ? 0 : p.cu[p.batch];

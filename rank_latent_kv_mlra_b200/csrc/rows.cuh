@@ -107,9 +107,14 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // exponentials run) and a P buffer each; with one, two score buffers and one P buffer.
 // Scores and values are issued by two warps: an MMA holds its issuer up while the tensor pipe's short
 // queue is full, and each wait costs a few hundred clocks, which one warp's MMAs hide for the other.
-template <int DB_, int DR_, int KT_, int DV_, int NQ_, int CST_, int RST_>
+// VST > 0: the per-head form. Keys and values are two buffers (a head's own, formed by the expansion
+// kernel), so values have a ring of VST places of their own, and a tile's keys and RoPE columns are
+// done with as soon as its scores are formed. A row tile is then 128 tokens of one head.
+template <int DB_, int DR_, int KT_, int DV_, int NQ_, int CST_, int RST_, int VST_ = 0>
 struct RowShape {
-  static constexpr int DB = DB_, DR = DR_, KT = KT_, DV = DV_, NQ = NQ_, CST = CST_, RST = RST_;
+  static constexpr int DB = DB_, DR = DR_, KT = KT_, DV = DV_, NQ = NQ_, CST = CST_, RST = RST_,
+                       VST = VST_;
+  static constexpr bool SPLIT = VST > 0;
   static constexpr int HALVES = DB / DV;
   static constexpr int ROWS = 128 * NQ;     // query rows a unit
   static constexpr int CW = DB < 64 ? DB : 64, NC = DB / CW, C_ROWB = CW * 2;
@@ -118,6 +123,8 @@ struct RowShape {
   static constexpr int Q_BYTES = NC * QC_REG + NR * QR_REG;
   static constexpr int KC_REG = KT * C_ROWB, KR_REG = KT * R_ROWB;
   static constexpr int C_BYTES = NC * KC_REG, R_BYTES = NR * KR_REG;
+  static constexpr int V_BYTES = (DV / CW) * KC_REG;
+  static constexpr int PST = SPLIT ? VST : CST;  // places of the ring that holds the values
   static constexpr int PAGE_TX = kPage * (DB + DR) * 2;
   static constexpr int SB = NQ == 1 ? 2 : 1;                  // score buffers
   static constexpr int S_COL = 0;
@@ -132,10 +139,11 @@ struct RowShape {
   static constexpr bool REGS = NQ == 2;
   static constexpr int PARTS = 4;            // unit parts handed out ahead
   static constexpr int READERS = 4 * NQ + 4; // warps that read them
-  static constexpr int NBARS = 4 * CST + RST + 2 * NQ + 4 + 3 * NQ + 2 + 2 * PARTS;
+  static constexpr int NBARS = 4 * CST + RST + 2 * VST + 2 * NQ + 4 + 3 * NQ + 2 + 2 * PARTS;
   static constexpr int OFF_C = NQ * Q_BYTES;
   static constexpr int OFF_R = OFF_C + CST * C_BYTES;
-  static constexpr int OFF_BAR = OFF_R + RST * R_BYTES;
+  static constexpr int OFF_V = OFF_R + RST * R_BYTES;
+  static constexpr int OFF_BAR = OFF_V + VST * V_BYTES;
   static constexpr int OFF_PARTS = (OFF_BAR + NBARS * 8 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_PARTS + PARTS * 48 + 64 + 1024;
   static_assert(SMEM <= 227 * 1024 && TMEM_USED <= 512, "shared and tensor memory of one CTA");
@@ -144,6 +152,7 @@ struct RowShape {
   static_assert(Q_BYTES % 1024 == 0 && C_BYTES % 1024 == 0 && R_BYTES % 1024 == 0 && KC_REG % 1024 == 0 &&
                     QC_REG % 1024 == 0 && KR_REG % 1024 == 0 && QR_REG % 1024 == 0,
                 "swizzled regions start on 1024 bytes");
+  static_assert(!SPLIT || (HALVES == 1 && RST == CST && VST <= CST), "per-head form");
   static_assert(RST <= CST && (NQ == 1 || CST >= 2), "a tile's full barrier counts both rings");
 };
 
@@ -160,9 +169,11 @@ struct RowParams {
   int d_c;
   float s_scale;           // from a score (packed query times staged row) to log2 units
   float o_scale;           // value of a staged latent element (1, or the E4M3 cache's scale)
+  int kv_rows;             // per-head form: rows of a head's key / value buffer (pt_stride pages a sequence)
   __nv_bfloat16* o_bf16;   // [tokens][vh][DB], or null
   float* o_f32;            // [tokens][vh][DB] when o_bf16 is null
-  float* lse;              // [tokens][vh] or null: natural log beside o_bf16, log2 beside o_f32
+  float* lse;              // [tokens][vh] or null
+  float lse_mul;           // from log2 to what lse holds
   float* part_o;           // [2 * CTAs][ROWS][DV]
   float* part_lse;         // [2 * CTAs][ROWS] log2
   int* status;
@@ -198,13 +209,15 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
     mlra_rows_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_r,
                      const __grid_constant__ CUtensorMap map_qc, const __grid_constant__ CUtensorMap map_qr,
                      const RowParams p) {
-  constexpr int NQ = Sh::NQ, KT = Sh::KT, CST = Sh::CST, RST = Sh::RST, DV = Sh::DV;
+  constexpr int NQ = Sh::NQ, KT = Sh::KT, CST = Sh::CST, RST = Sh::RST, VST = Sh::VST, PST = Sh::PST, DV = Sh::DV;
+  constexpr bool SPLIT = Sh::SPLIT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* qbuf = smem;
   uint8_t* cring = smem + Sh::OFF_C;
   uint8_t* rring = smem + Sh::OFF_R;
+  uint8_t* vring = smem + (SPLIT ? Sh::OFF_V : Sh::OFF_C);  // the values
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + Sh::OFF_BAR);  // [CST] a key tile has landed
   uint64_t* cempty = kfull + CST;        // [CST] its block columns are done with
   uint64_t* rempty = cempty + CST;       // [RST] its RoPE columns are
@@ -220,7 +233,9 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
   uint64_t* patch = ofree + NQ;          // [CST] a key tile is ready to be patched
   uint64_t* patched = patch + CST;       // [CST] and has been
   uint64_t* drained = patched + CST;     // [2]
-  uint64_t* pready = drained + 2;        // [PARTS]
+  uint64_t* vfull = drained + 2;         // [VST] per-head form: values have landed
+  uint64_t* vempty = vfull + VST;        // [VST] and are done with
+  uint64_t* pready = vempty + VST;        // [PARTS]
   uint64_t* pread = pready + Sh::PARTS;  // [PARTS]
   int4* parts = reinterpret_cast<int4*>(smem + Sh::OFF_PARTS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(parts + 3 * Sh::PARTS);
@@ -234,6 +249,10 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       mbar_init(&cempty[s], 1);
       mbar_init(&patch[s], 1);
       mbar_init(&patched[s], 1);
+    }
+    for (int s = 0; s < VST; ++s) {
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], 1);
     }
     for (int s = 0; s < RST; ++s) mbar_init(&rempty[s], 1);
     for (int q = 0; q < 2; ++q) {
@@ -306,14 +325,73 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       const uint64_t pol = l2_policy_evict_last();
       uint32_t issued = 0, parity = 0;     // key tiles' full barriers
       uint32_t q_issued = 0, q_parity = 0; // query barriers
+      uint32_t v_issued = 0, v_parity = 0; // values' full barriers
       uint32_t qc[NQ];                     // query loads so far, a row tile
 #pragma unroll
       for (int q = 0; q < NQ; ++q) qc[q] = 0;
+      // the part's queries (behind its first key tile, whose place is free earlier); one lane
+      auto load_queries = [&](int sub, int nrow) {
+        const int rows = p.heads_tile * p.tok_tile;
+        for (int q = 0; q < nrow; ++q) {
+          if (!mbar_wait(&qempty[q], (qc[q] & 1) ^ 1, abort_flag, p.wait_limit_ns)) return false;
+          mbar_arrive_expect_tx(&qfull[q], rows * (Sh::DB + Sh::DR) * 2);
+          q_issued |= 1u << q;
+          q_parity = (q_parity & ~(1u << q)) | ((qc[q] & 1) << q);
+          ++qc[q];
+          uint8_t* dst = qbuf + q * Sh::Q_BYTES;
+          const int tok = u.t.tok0 + q * p.tok_tile;
+          for (int r = 0; r < Sh::NC; ++r)
+            tma_load_4d(dst + r * Sh::QC_REG, &map_qc, &qfull[q], r * Sh::CW, 0, sub, tok, pol);
+          for (int r = 0; r < Sh::NR; ++r)
+            tma_load_4d(dst + Sh::NC * Sh::QC_REG + r * Sh::QR_REG, &map_qr, &qfull[q], Sh::DB + r * Sh::RW, 0, sub,
+                        tok, pol);
+        }
+        return true;
+      };
+      auto note = [&](uint32_t& mask, uint32_t& par, int s, uint32_t ph) {
+        mask |= 1u << s;
+        par = (par & ~(1u << s)) | (ph << s);
+      };
       bool ok = true;
       while (ok && take(u)) {
         const int sub = u.sub / Sh::HALVES;
-        const int blk = sub / p.chunks;
         const int nrow = rows_of(u);
+        if constexpr (SPLIT) {
+          // keys a tile ahead of values, whose place comes free later
+          const int r0 = u.t.b * p.pt_stride * kPage, y0 = sub * p.kv_rows + r0;
+          if (lane == 0) {
+            auto load_keys = [&](int t, uint32_t n) {
+              const int s = n % CST;
+              const uint32_t ph = (n / CST) & 1;
+              if (!mbar_wait(&cempty[s], ph ^ 1, abort_flag, p.wait_limit_ns)) return false;
+              mbar_arrive_expect_tx(&kfull[s], Sh::C_BYTES + Sh::R_BYTES);
+              note(issued, parity, s, ph);
+              for (int r = 0; r < Sh::NC; ++r)
+                tma_load_2d(cring + s * Sh::C_BYTES + r * Sh::KC_REG, &map_c, &kfull[s], r * Sh::CW, y0 + t * KT, pol);
+              for (int r = 0; r < Sh::NR; ++r)
+                tma_load_2d(rring + s * Sh::R_BYTES + r * Sh::KR_REG, &map_r, &kfull[s], r * Sh::RW, r0 + t * KT, pol);
+              return true;
+            };
+            ok = load_keys(u.begin, kt) && load_queries(sub, nrow);
+            for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
+              if (t + 1 < u.end) ok = load_keys(t + 1, kt + 1);
+              const int s = kt % PST;
+              const uint32_t ph = (kt / PST) & 1;
+              ok = ok && mbar_wait(&vempty[s], ph ^ 1, abort_flag, p.wait_limit_ns);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&vfull[s], Sh::V_BYTES);
+              note(v_issued, v_parity, s, ph);
+              for (int r = 0; r < DV / Sh::CW; ++r)
+                tma_load_2d(vring + s * Sh::V_BYTES + r * Sh::KC_REG, &map_c, &vfull[s], Sh::DB + r * Sh::CW,
+                            y0 + t * KT, pol);
+              // (the patch warp may look at this phase of vfull only now)
+              if ((t + 1) * KT > u.t.lim0) mbar_arrive(&patch[s]);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          continue;
+        }
+        const int blk = sub / p.chunks;
         const int pages = (tile_limit(u.t, p.causal) + kPage - 1) / kPage;
         const size_t row = (size_t)u.t.b * p.pt_stride;
         constexpr int PPT = KT / kPage;  // pages a key tile
@@ -343,8 +421,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
                  mbar_wait(&rempty[rs], ((kt / RST) & 1) ^ 1, abort_flag, p.wait_limit_ns);
             if (ok) {
               mbar_arrive_expect_tx(&kfull[s], npg * Sh::PAGE_TX);
-              issued |= 1u << s;
-              parity = (parity & ~(1u << s)) | (ph << s);
+              note(issued, parity, s, ph);
 #pragma unroll
               for (int x = 0; x < PPT; ++x) {
                 if (x >= npg) break;
@@ -361,25 +438,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
                               p.d_c + r * Sh::RW, y, pol);
               }
             }
-            // the part's queries, behind its first key tile (whose place is free earlier)
-            if (t == u.begin) {
-              const int rows = p.heads_tile * p.tok_tile;
-              for (int q = 0; q < nrow && ok; ++q) {
-                ok = mbar_wait(&qempty[q], (qc[q] & 1) ^ 1, abort_flag, p.wait_limit_ns);
-                if (!ok) break;
-                mbar_arrive_expect_tx(&qfull[q], rows * (Sh::DB + Sh::DR) * 2);
-                q_issued |= 1u << q;
-                q_parity = (q_parity & ~(1u << q)) | ((qc[q] & 1) << q);
-                ++qc[q];
-                uint8_t* dst = qbuf + q * Sh::Q_BYTES;
-                const int tok = u.t.tok0 + q * p.tok_tile;
-                for (int r = 0; r < Sh::NC; ++r)
-                  tma_load_4d(dst + r * Sh::QC_REG, &map_qc, &qfull[q], r * Sh::CW, 0, sub, tok, pol);
-                for (int r = 0; r < Sh::NR; ++r)
-                  tma_load_4d(dst + Sh::NC * Sh::QC_REG + r * Sh::QR_REG, &map_qr, &qfull[q], Sh::DB + r * Sh::RW, 0,
-                              sub, tok, pol);
-              }
-            }
+            if (t == u.begin) ok = ok && load_queries(sub, nrow);
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
         }
@@ -392,6 +451,9 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         for (int q = 0; q < NQ; ++q)
           if ((q_issued >> q) & 1)
             if (!mbar_wait_drain(&qfull[q], (q_parity >> q) & 1, p.wait_limit_ns)) *drain_err = 1;
+        for (int s = 0; s < VST; ++s)
+          if ((v_issued >> s) & 1)
+            if (!mbar_wait_drain(&vfull[s], (v_parity >> s) & 1, p.wait_limit_ns)) *drain_err = 1;
       }
     } else if (warp == Sh::QK_WARP) {
       // ------------------------------ scores ------------------------------
@@ -446,10 +508,10 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
               umma_commit(&sfull[NQ == 1 ? kt & 1 : q]);
               if (i == n - 1) umma_commit(&qempty[q]);
               if (q == nrow - 1) {
-                umma_commit(&rempty[kt % RST]);
+                umma_commit(SPLIT ? &cempty[kt % CST] : &rempty[kt % RST]);
                 // a tile that reaches past what the part's first token sees is patched (see the patch
                 // warp) between its score MMAs and its value MMAs
-                if ((u.begin + i + 1) * KT > u.t.lim0) umma_commit(&patch[kt % CST]);
+                if (!SPLIT && (u.begin + i + 1) * KT > u.t.lim0) umma_commit(&patch[kt % PST]);
               }
             }
           }
@@ -463,7 +525,8 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       const bool one = elect_lane();
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV, false, true);
       constexpr uint32_t c_hi = desc_hi(8 * Sh::C_ROWB, swizzle_code(Sh::C_ROWB));
-      const uint32_t v_lo = desc_lo(smem_u32(cring), Sh::KC_REG);
+      const uint32_t v_lo = desc_lo(smem_u32(vring), Sh::KC_REG);
+      constexpr uint32_t place = (SPLIT ? Sh::V_BYTES : Sh::C_BYTES) >> 4;
       uint32_t pc[NQ], oc[NQ];  // P tiles and parts so far
 #pragma unroll
       for (int q = 0; q < NQ; ++q) pc[q] = oc[q] = 0;
@@ -472,14 +535,15 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         const int n = u.end - u.begin, nrow = rows_of(u);
         const uint32_t half = (u.sub % Sh::HALVES) * ((DV / Sh::CW) * (Sh::KC_REG >> 4));
         for (int i = 0; i < n && ok; ++i, ++kt) {
+          if constexpr (SPLIT) ok = wait(&vfull[kt % PST], (kt / PST) & 1);
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             if (q >= nrow || !ok) break;
             ok = wait(&pfull[q], pc[q] & 1);
             ++pc[q];
             if (q == 0 && (u.begin + i + 1) * KT > u.t.lim0) {
-              ok = ok && wait(&patched[kt % CST], (fixes >> (kt % CST)) & 1);
-              fixes ^= 1u << (kt % CST);
+              ok = ok && wait(&patched[kt % PST], (fixes >> (kt % PST)) & 1);
+              fixes ^= 1u << (kt % PST);
             }
             if (i == 0) {
               ok = ok && wait(&ofree[q], (oc[q] & 1) ^ 1);
@@ -487,7 +551,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
             }
             if (!ok) break;
             tc_fence_after();
-            const uint32_t b0 = v_lo + (kt % CST) * (Sh::C_BYTES >> 4) + half;
+            const uint32_t b0 = v_lo + (kt % PST) * place + half;
             const uint32_t a = tbase + Sh::P_COL + q * (KT / 2);
             if (one) {
 #pragma unroll
@@ -496,7 +560,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
                         (i > 0 || ks > 0) ? 1u : 0u);
               umma_commit(&pvdone[q]);
               // (every score of the tile was formed before the last row tile's P)
-              if (q == nrow - 1) umma_commit(&cempty[kt % CST]);
+              if (q == nrow - 1) umma_commit(SPLIT ? &vempty[kt % PST] : &cempty[kt % PST]);
             }
           }
         }
@@ -514,12 +578,23 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       // This warp also walks the plan and hands the unit parts out, two ahead of the one it is at.
       const int tiles = __ldg(p.plan.hdr);
       UnitWalk walk;
-      walk.init(&p.plan, tiles, stretch_of(__ldg(p.plan.start + tiles), blockIdx.x, gridDim.x), p.nsub * Sh::HALVES,
-                KT, p.causal);
+      const Stretch st = stretch_of(__ldg(p.plan.start + tiles), blockIdx.x, gridDim.x);
+      walk.init(&p.plan, tiles, st, p.nsub * Sh::HALVES, KT, p.causal);
       uint32_t given = 0;
       bool more = true;
       auto give = [&]() {
         const UnitPart g = walk.next();
+        if (given == 0 && lane == 0) {
+          // for the merge: the unit that this stretch goes on with, and the CTAs that share it
+          int c0 = -1, c1 = -1;
+          if (g.valid && g.begin > 0) {
+            const long long first = walk.at + (long long)g.sub * unit_cost(g.kv) + kUnitCost;
+            c0 = (int)(first / st.quota);
+            c1 = (int)((first + g.kv - 1) / st.quota);
+          }
+          p.plan.cut[2 * blockIdx.x] = make_int4(c0, c1, g.sub, 0);
+          p.plan.cut[2 * blockIdx.x + 1] = make_int4(g.t.tok0, g.t.ntok, 0, 0);
+        }
         const int e = given % Sh::PARTS;
         if (!wait(&pread[e], ((given / Sh::PARTS) & 1) ^ 1)) return false;
         if (lane == 0) {
@@ -541,16 +616,18 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         const int lim = tile_limit(u.t, p.causal);
         for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
           if ((t + 1) * KT <= u.t.lim0) continue;
-          // the MMAs that form this key tile's scores have read it (and it had landed)
-          ok = wait(&patch[kt % CST], (fixes >> (kt % CST)) & 1) && wait(&kfull[kt % CST], (kt / CST) & 1);
+          // the MMAs that form this key tile's scores have read it (and it had landed); per-head form:
+          // its values have been asked for, and land
+          ok = wait(&patch[kt % PST], (fixes >> (kt % PST)) & 1) &&
+               (SPLIT ? wait(&vfull[kt % PST], (kt / PST) & 1) : wait(&kfull[kt % PST], (kt / PST) & 1));
           if (!ok) break;
-          fixes ^= 1u << (kt % CST);
-          uint8_t* st_mem = cring + (kt % CST) * Sh::C_BYTES;
+          fixes ^= 1u << (kt % PST);
+          uint8_t* st_mem = vring + (kt % PST) * (SPLIT ? Sh::V_BYTES : Sh::C_BYTES);
           const int k0 = t * KT;
           const int some = max(0, min(KT, max(u.t.lim0, 0) - k0));  // rows [some, none) only some tokens see
           const int none = max(0, min(KT, lim - k0));
           constexpr int CPR = Sh::C_ROWB / 16;
-          for (int r = 0; r < Sh::NC; ++r) {
+          for (int r = 0; r < (SPLIT ? DV / Sh::CW : Sh::NC); ++r) {
             uint8_t* reg = st_mem + r * Sh::KC_REG;
             for (int i = none * CPR + lane; i < KT * CPR; i += 32)
               *reinterpret_cast<uint4*>(reg + i * 16) = make_uint4(0, 0, 0, 0);
@@ -568,7 +645,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&patched[kt % CST]);
+          if (lane == 0) mbar_arrive(&patched[kt % PST]);
         }
       }
     }
@@ -700,7 +777,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         if (!whole)
           p.part_lse[pat] = lse2;
         else if (half == 0 && p.lse != nullptr)
-          p.lse[at] = p.o_bf16 != nullptr ? lse2 * kLn2 : lse2;
+          p.lse[at] = lse2 * p.lse_mul;
       }
       __nv_bfloat16* const out = p.o_bf16 + ((size_t)u.t.tok0 * p.vh + head0) * Sh::DB + half * DV;
 #pragma unroll 1
@@ -720,10 +797,26 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             if (tok4[r] < u.t.ntok) *reinterpret_cast<uint4*>(out + off4[r] + c) = v4[r];
-        } else if (mine) {
-          float4* dst = reinterpret_cast<float4*>(whole ? p.o_f32 + at * Sh::DB + half * DV + c : p.part_o + pat * DV + c);
+        } else {
+          // fp32: 16 columns at a time, 64 bytes of a row together
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int g = 0; g < 2; ++g) {
+            uint4 v4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v4[e] = make_uint4(__float_as_uint(o[16 * g + 4 * e]), __float_as_uint(o[16 * g + 4 * e + 1]),
+                                 __float_as_uint(o[16 * g + 4 * e + 2]), __float_as_uint(o[16 * g + 4 * e + 3]));
+            exchange4(v4, lane);
+            const int x = c + 16 * g + (lane & 3) * 4;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if (tok4[r] >= u.t.ntok) continue;
+              float* dst = whole ? p.o_f32 + ((size_t)u.t.tok0 * p.vh + head0) * Sh::DB + half * DV + off4[r] -
+                                       (lane & 3) * 8 + x
+                                 : p.part_o + (pat - (lane & 3) + r) * DV + x;
+              *reinterpret_cast<uint4*>(dst) = v4[r];
+            }
+          }
         }
         __syncwarp();
       }
@@ -750,59 +843,51 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
 // ---------------------------------------------------------------------------------------
 struct MergeParams {
   RowPlan plan;
-  int ctas;                // grid of the attention kernel
-  int causal, key_tile, units, halves, nsub, chunks, heads_tile, tok_tile, heads_block, vh, db, dv, rows;
+  int causal, key_tile, halves, chunks, heads_tile, tok_tile, heads_block, vh, db, dv, rows;
   const float* part_o;
   const float* part_lse;
-  __nv_bfloat16* o_bf16;   // [tokens][vh][db]
+  __nv_bfloat16* o_bf16;   // [tokens][vh][db], or null
+  float* o_f32;            // the same when o_bf16 is null
   float* lse;              // natural log, or null
 };
 
-// Grid (ctas, row slices). Block (c, s) looks after the boundary at the start of CTA c's stretch: if it
-// is the first boundary inside a unit, the unit's parts (CTAs c - 1, c, ... in that order) are
-// merged by log-sum-exp. A warp takes a row, a lane dv / 32 features.
+// Grid (CTAs of the attention kernel, row slices). Block (c, s) looks after the unit that CTA c goes on
+// with, if CTA c - 1 began it: the unit's parts (CTAs c - 1, c, ... in that order) are merged by
+// log-sum-exp. A warp takes a row, a lane dv / 32 features. Bound by latency: a few hundred rows a
+// block column, two loads deep.
 __global__ void __launch_bounds__(256) mlra_rows_merge_kernel(const MergeParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int tiles = __ldg(p.plan.hdr);
-  const long long total = __ldg(p.plan.start + tiles);
   const int warp = warp_id(), lane = lane_id(), nwarp = blockDim.x >> 5;
   const int slice = blockIdx.y * nwarp + warp, slices = gridDim.y * nwarp;
-  // token tiles without a key: zeros
-  for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
-    const TokenTile t = p.plan.tile[i];
-    if (key_tiles(t, p.causal, p.key_tile) > 0) continue;
-    for (long long r = slice; r < (long long)t.ntok * p.vh; r += slices) {
-      const size_t at = (size_t)t.tok0 * p.vh + r;
-      for (int f = lane * 2; f < p.db; f += 64) *reinterpret_cast<uint32_t*>(p.o_bf16 + at * p.db + f) = 0u;
-      if (lane == 0 && p.lse != nullptr) p.lse[at] = -INFINITY;
+  auto put = [&](size_t at, float v) {
+    if (p.o_bf16 != nullptr) p.o_bf16[at] = __float2bfloat16_rn(v);
+    else p.o_f32[at] = v;
+  };
+  if (__ldg(p.plan.hdr + 3) > 0) {
+    // token tiles without a key: zeros
+    const int tiles = __ldg(p.plan.hdr);
+    for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
+      const TokenTile t = p.plan.tile[i];
+      if (key_tiles(t, p.causal, p.key_tile) > 0) continue;
+      for (long long r = slice; r < (long long)t.ntok * p.vh; r += slices) {
+        const size_t at = (size_t)t.tok0 * p.vh + r;
+        for (int f = lane; f < p.db; f += 32) put(at * p.db + f, 0.f);
+        if (lane == 0 && p.lse != nullptr) p.lse[at] = -INFINITY;
+      }
     }
   }
   const int c = blockIdx.x;
-  const Stretch st = stretch_of(total, c, p.ctas);
-  if (c == 0 || st.lo >= total) return;
-  int lo = 0, up = tiles;  // the tile that holds position st.lo
-  while (up - lo > 1) {
-    const int mid = (lo + up) >> 1;
-    if (__ldg(p.plan.start + mid) <= st.lo) lo = mid;
-    else up = mid;
-  }
-  const TokenTile t = p.plan.tile[lo];
-  const int kv = key_tiles(t, p.causal, p.key_tile);
-  const int cost = unit_cost(kv);
-  const long long at0 = __ldg(p.plan.start + lo);
-  const int usub = (int)((st.lo - at0) / cost);
-  const long long first = at0 + (long long)usub * cost + kUnitCost, last = first + kv - 1;  // its key tiles
-  if (st.lo <= first || st.lo > last) return;  // the boundary does not cut the unit's key tiles
-  const int c0 = (int)(first / st.quota), c1 = (int)(last / st.quota);
-  if (c0 != c - 1) return;                     // not the first boundary in it
-  const int sub = usub / p.halves, half = usub % p.halves;
+  const int4 cut = __ldg(p.plan.cut + 2 * c), tk = __ldg(p.plan.cut + 2 * c + 1);
+  const int c0 = cut.x, c1 = cut.y, ntok = tk.y;
+  if (c == 0 || c0 != c - 1) return;
+  const int sub = cut.z / p.halves, half = cut.z % p.halves;
   const int per = p.dv / 32;
   for (int r = slice; r < p.rows; r += slices) {
     const int q = r >> 7, row = r & 127;
     const int tl = row / p.heads_tile, hr = row - tl * p.heads_tile;
     const int tok = q * p.tok_tile + tl;
-    if (tl >= p.tok_tile || tok >= t.ntok) continue;
+    if (tl >= p.tok_tile || tok >= ntok) continue;
     float mx = -INFINITY, sum = 0.f;
     float acc[8];
 #pragma unroll
@@ -823,10 +908,10 @@ __global__ void __launch_bounds__(256) mlra_rows_merge_kernel(const MergeParams 
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int head = (sub / p.chunks) * p.heads_block + (sub % p.chunks) * p.heads_tile + hr;
-    const size_t at = (size_t)(t.tok0 + tok) * p.vh + head;
+    const size_t at = (size_t)(tk.x + tok) * p.vh + head;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < per) p.o_bf16[at * p.db + half * p.dv + e * 32 + lane] = __float2bfloat16_rn(acc[e] * inv);
+      if (e < per) put(at * p.db + half * p.dv + e * 32 + lane, acc[e] * inv);
     if (lane == 0 && half == 0 && p.lse != nullptr)
       p.lse[at] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * kLn2;
   }
@@ -858,6 +943,10 @@ struct UpShape {
   static_assert(W_BYTES % 1024 == 0 && A_REG % 1024 == 0 && SMEM <= 227 * 1024, "layout");
 };
 
+// EXPAND: the same product over cached rows instead, for the per-head form: each head's keys c_j W^UK_h
+// and values c_j W^UV_h of every cached token, [head][row][K | V], row = b * pt_stride * page + token; a
+// weight is then one of a head's two. Reads the rows once a weight (from L2 after the first),
+// writes 512 bytes a token and head. The blocks also copy the RoPE columns to rows of their own.
 struct UpParams {
   const int* used;       // tokens in use (rows past them are left as they were)
   void* out;             // [tokens][heads][DH]
@@ -865,12 +954,20 @@ struct UpParams {
   float out_scale;
   int* status;
   unsigned long long wait_limit_ns;
+  // EXPAND
+  EarlyTags tags;
+  const int* lens;
+  const int* page_table;
+  int pt_stride, batch, num_pages, heads_block, kv_rows, width, d_c, d_r;
+  const __nv_bfloat16* pool;
+  __nv_bfloat16* kv;     // [heads][kv_rows][2 * DH]
+  __nv_bfloat16* kr;     // [kv_rows][d_r]
 };
 
-template <class Sh>
+template <class Sh, bool EXPAND = false>
 __global__ void __launch_bounds__(Sh::THREADS)
-    mlra_rows_up_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_o,
-                        const UpParams p) {
+    mlra_rows_up_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_w2,
+                        const __grid_constant__ CUtensorMap map_o, const UpParams p) {
   constexpr int DH = Sh::DH, STAGES = Sh::STAGES, NKC = Sh::NKC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -915,9 +1012,16 @@ __global__ void __launch_bounds__(Sh::THREADS)
   const uint32_t tbase = *tmem_slot;
   grid_launch_dependents();
 
-  const int used = __ldg(p.used);
-  const int tiles = (used + 127) / 128;
-  const long long items = (long long)tiles * p.heads;
+  if (EXPAND && blockIdx.x == 0 && threadIdx.x == 0) clear_status_and_tags(p.status, p.tags);
+  const int used = EXPAND ? 0 : __ldg(p.used);
+  const int seq_tiles = EXPAND ? (p.pt_stride + 1) / 2 : 1;  // token tiles of a sequence's table row
+  const int tiles = EXPAND ? p.batch * seq_tiles : (used + 127) / 128;
+  const long long items = (long long)tiles * p.heads * (EXPAND ? 2 : 1);
+  auto length = [&](int b) { return min(max(__ldg(p.lens + b), 0), p.pt_stride * kPage); };
+  // EXPAND: whether the tile lies past its sequence's end
+  auto skip = [&](int tile) {
+    return EXPAND && (tile % seq_tiles) * 128 >= length(tile / seq_tiles);
+  };
   const long long per = (items + gridDim.x - 1) / gridDim.x;
   const long long lo = min(per * blockIdx.x, items), hi = min(lo + per, items);
 
@@ -928,7 +1032,20 @@ __global__ void __launch_bounds__(Sh::THREADS)
       int w_parity = -1, head = -1;
       bool ok = true;
       for (long long it = lo; it < hi && ok; ++it) {
-        const int h = (int)(it / tiles), tok = (int)(it % tiles) * 128;
+        const int h = (int)(it / tiles), tile = (int)(it % tiles), tok = tile * 128;
+        if (skip(tile)) continue;
+        int id0 = 0, id1 = 0;  // EXPAND: the tile's two pages (the second may not exist)
+        if (EXPAND) {
+          const int b = tile / seq_tiles, pg = (tile % seq_tiles) * 2;
+          const int* row = p.page_table + (size_t)b * p.pt_stride;
+          id0 = __ldg(row + pg);
+          id1 = (pg + 1) * kPage < length(b) ? __ldg(row + pg + 1) : id0;
+          if (id0 < 0 || id0 >= p.num_pages || id1 < 0 || id1 >= p.num_pages) {
+            report_early(p.tags, kTagPageOob);
+            id0 = id0 < 0 || id0 >= p.num_pages ? 0 : id0;
+            id1 = id1 < 0 || id1 >= p.num_pages ? 0 : id1;
+          }
+        }
         if (h != head) {
           head = h;
           ok = mbar_wait(wfree, (wc & 1) ^ 1, abort_flag, p.wait_limit_ns);
@@ -938,8 +1055,8 @@ __global__ void __launch_bounds__(Sh::THREADS)
           for (int a = 0; a < Sh::NATOM; ++a)
             for (int j = 0; j < Sh::SUMK; ++j)
               for (int r = 0; r < Sh::DBB; r += Sh::WBOX)
-                tma_load_2d(wbuf + a * Sh::ATOM + (j * Sh::DBB + r) * Sh::WROWB, &map_w, wfull, a * Sh::AW,
-                            (j * p.heads + h) * Sh::DBB + r, keep);
+                tma_load_2d(wbuf + a * Sh::ATOM + (j * Sh::DBB + r) * Sh::WROWB, EXPAND && (h & 1) ? &map_w2 : &map_w,
+                            wfull, a * Sh::AW, (EXPAND ? h / 2 : j * p.heads + h) * Sh::DBB + r, keep);
           ++wc;
         }
         for (int kc = 0; kc < NKC && ok; ++kc, ++c) {
@@ -951,6 +1068,12 @@ __global__ void __launch_bounds__(Sh::THREADS)
           issued |= 1u << s;
           parity = (parity & ~(1u << s)) | (ph << s);
           const int f = kc * Sh::CW;
+          if (EXPAND) {
+            const int x = (h / 2 / p.heads_block) * Sh::DBB + f;
+            tma_load_2d(ring + s * Sh::A_REG, &map_o, &full[s], x, id0 * kPage, keep);
+            tma_load_2d(ring + s * Sh::A_REG + kPage * Sh::ROWB, &map_o, &full[s], x, id1 * kPage, keep);
+            continue;
+          }
           tma_load_3d(ring + s * Sh::A_REG, &map_o, &full[s], f % Sh::DBB, (f / Sh::DBB) * p.heads + h, tok, pol);
         }
       }
@@ -967,9 +1090,12 @@ __global__ void __launch_bounds__(Sh::THREADS)
       uint32_t c = 0, wc = 0, n = 0;
       int head = -1;
       bool ok = true;
-      for (long long it = lo; it < hi && ok; ++it, ++n) {
+      for (long long it = lo; it < hi && ok; ++it) {
         const int h = (int)(it / tiles);
+        if (skip((int)(it % tiles))) continue;
         if (h != head) {
+          // the last head's MMAs free its weight
+          if (head >= 0) umma_commit(wfree);
           head = h;
           ok = mbar_wait(wfull, wc & 1, abort_flag, p.wait_limit_ns);
           if (!ok) break;
@@ -992,7 +1118,7 @@ __global__ void __launch_bounds__(Sh::THREADS)
         }
         if (!ok) break;
         umma_commit(&dfull[n & 1]);
-        if (it + 1 < hi && (int)((it + 1) / tiles) != head) umma_commit(wfree);
+        ++n;
       }
       umma_commit(drained);
       if (!mbar_wait_drain(drained, 0, p.wait_limit_ns)) *drain_err = 1;
@@ -1002,8 +1128,24 @@ __global__ void __launch_bounds__(Sh::THREADS)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     uint32_t n = 0;
-    for (long long it = lo; it < hi; ++it, ++n) {
-      const int h = (int)(it / tiles), tok = (int)(it % tiles) * 128 + row;
+    if constexpr (EXPAND) {
+      // RoPE columns of the pages, 16 bytes a thread
+      const int cpr = p.d_r / 8, tid = threadIdx.x - 64;
+      for (int pg = blockIdx.x; pg < p.batch * p.pt_stride; pg += gridDim.x) {
+        const int b = pg / p.pt_stride;
+        if ((pg - b * p.pt_stride) * kPage >= length(b)) continue;
+        int id = __ldg(p.page_table + pg);
+        if (id < 0 || id >= p.num_pages) id = 0;  // (reported by the loads)
+        for (int i = tid; i < kPage * cpr; i += 128) {
+          const int r = i / cpr, x = (i % cpr) * 8;
+          *reinterpret_cast<uint4*>(p.kr + ((size_t)pg * kPage + r) * p.d_r + x) = __ldg(
+              reinterpret_cast<const uint4*>(p.pool + ((size_t)id * kPage + r) * p.width + p.d_c + x));
+        }
+      }
+    }
+    for (long long it = lo; it < hi; ++it) {
+      const int h = (int)(it / tiles), tile = (int)(it % tiles), tok = tile * 128 + row;
+      if (skip(tile)) continue;
       if (!__all_sync(0xffffffffu, mbar_wait(&dfull[n & 1], (n >> 1) & 1, abort_flag, p.wait_limit_ns))) break;
       tc_fence_after();
 #pragma unroll
@@ -1011,10 +1153,26 @@ __global__ void __launch_bounds__(Sh::THREADS)
         float v[32];
         tmem_load_row<32>(tbase + lane_base + (n & 1) * DH + c, v);
         tmem_ld_wait();
+        if constexpr (!EXPAND) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] *= p.out_scale;
-        // rows behind the last sequence (tok >= used) stay as they were
-        if (p.out_f32) {
+          for (int e = 0; e < 32; ++e) v[e] *= p.out_scale;
+        }
+        if constexpr (EXPAND) {
+          // the sequence's rows end with its table row, within the tile where that has an odd page
+          uint4 v4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v4[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                               pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+          exchange4(v4, lane);
+          const int b = tile / seq_tiles, t0 = (tile % seq_tiles) * 128 + (row & ~3);
+          __nv_bfloat16* dst = p.kv + ((size_t)(h / 2) * p.kv_rows + (size_t)b * p.pt_stride * kPage + t0) * (2 * DH) +
+                               (h & 1) * DH + c + (lane & 3) * 8;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (t0 + r < p.pt_stride * kPage) *reinterpret_cast<uint4*>(dst + (size_t)r * 2 * DH) = v4[r];
+        } else if (p.out_f32) {
+          // (rows behind the last sequence, tok >= used, stay as they were)
           float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((size_t)tok * p.heads + h) * DH + c);
           if (tok < used) {
 #pragma unroll
@@ -1038,13 +1196,19 @@ __global__ void __launch_bounds__(Sh::THREADS)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&dfree[n & 1]);
+      ++n;
     }
   }
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0) {
-    if (*abort_flag) set_status(p.status, kErrTimeout);
-    if (*drain_err) force_status(p.status, kErrDrain);
+    if (EXPAND) {  // the call's first kernel: block 0 may not have cleared the status word yet
+      if (*abort_flag) report_early(p.tags, kTagTimeout);
+      if (*drain_err) report_early(p.tags, kTagDrain);
+    } else {
+      if (*abort_flag) set_status(p.status, kErrTimeout);
+      if (*drain_err) force_status(p.status, kErrDrain);
+    }
   }
   if (warp == 1) {
     tc_fence_after();

@@ -13,6 +13,9 @@ using RowsB128 = RowShape<128, 64, 128, 128, 2, 3, 2>;
 using RowsB256 = RowShape<256, 64, 64, 256, 1, 3, 3>;
 using RowsB512 = RowShape<512, 64, 64, 256, 1, 1, 1>;
 
+// The per-head form (whole prompts): keys of 128 + 64, values of 128, whatever the block width
+using RowsHead = RowShape<128, 64, 128, 128, 2, 2, 2, 1>;
+
 constexpr int kMaxQueryTokens = 1 << 21;  // grid rows of the absorb kernel
 
 template <class F>
@@ -29,6 +32,11 @@ template <int DBB, int DH, int SUMK>
 cudaError_t prep_up() {
   return prep_kernel(mlra_rows_up_kernel<UpShape<DBB, DH, SUMK>>, UpShape<DBB, DH, SUMK>::SMEM);
 }
+template <int DBB>
+cudaError_t prep_head() {
+  cudaError_t e = prep_kernel(mlra_rows_up_kernel<UpShape<DBB, 128, 1>, true>, UpShape<DBB, 128, 1>::SMEM);
+  return e == cudaSuccess ? prep_kernel(mlra_rows_kernel<RowsHead>, RowsHead::SMEM) : e;
+}
 cudaError_t prep_rows(Variant v) {
   cudaError_t e = with_rows(v, [](auto sh) {
     using Sh = decltype(sh);
@@ -39,11 +47,17 @@ cudaError_t prep_rows(Variant v) {
     case kTiny:
       e = prep_up<32, 32, 1>();
       return e == cudaSuccess ? prep_up<32, 32, 4>() : e;
-    case kMlra2: return prep_up<256, 128, 1>();
+    case kMlra2:
+      e = prep_up<256, 128, 1>();
+      return e == cudaSuccess ? prep_head<256>() : e;
     case kMlra2Sum: return prep_up<256, 128, 2>();
-    case kMla: return prep_up<512, 128, 1>();
+    case kMla:
+      e = prep_up<512, 128, 1>();
+      return e == cudaSuccess ? prep_head<512>() : e;
     case kMlra4Sum: return prep_up<128, 128, 4>();
-    default: return prep_up<128, 128, 1>();
+    default:
+      e = prep_up<128, 128, 1>();
+      return e == cudaSuccess && v == kMlra4 ? prep_head<128>() : e;
   }
 }
 
@@ -111,22 +125,34 @@ struct RowsWorkspace {
   float* part_o;
   float* part_lse;
 };
-// Plan and partial slots of the row attention over `tokens` query tokens of `seqs` sequences.
-RowsWorkspace carve_rows(const mlra_ctx* h, Carver& c, size_t tokens, size_t seqs, bool tok_tile) {
-  return with_rows(h->var, [&](auto sh) {
-    using Sh = decltype(sh);
-    const int heads = h->heads_block < h->np ? h->heads_block : h->np;
-    const size_t tile = (size_t)Sh::NQ * (128 / heads);
-    const size_t tiles = tokens / tile + seqs;
-    RowsWorkspace w;
-    w.plan.hdr = c.take<int>(4);
-    w.plan.start = c.take<long long>(tiles + 1);
-    w.plan.tile = c.take<TokenTile>(tiles);
-    w.plan.tok_tile = tok_tile ? c.take<int>(tokens) : nullptr;
-    w.part_lse = c.take<float>((size_t)2 * h->num_sms * Sh::ROWS);
-    w.part_o = c.take<float>((size_t)2 * h->num_sms * Sh::ROWS * Sh::DV);
-    return w;
-  });
+// Plan and partial slots of the row attention over `tokens` query tokens of `seqs` sequences;
+// `heads`: heads a row tile stacks.
+template <class Sh>
+RowsWorkspace carve_rows(const mlra_ctx* h, Carver& c, size_t tokens, size_t seqs, int heads, bool tok_tile) {
+  const size_t tile = (size_t)Sh::NQ * (128 / heads);
+  const size_t tiles = tokens / tile + seqs;
+  RowsWorkspace w;
+  w.plan.hdr = c.take<int>(4);
+  w.plan.start = c.take<long long>(tiles + 1);
+  w.plan.tile = c.take<TokenTile>(tiles);
+  w.plan.cut = c.take<int4>((size_t)2 * h->num_sms);
+  w.plan.tok_tile = tok_tile ? c.take<int>(tokens) : nullptr;
+  w.part_lse = c.take<float>((size_t)2 * h->num_sms * Sh::ROWS);
+  w.part_o = c.take<float>((size_t)2 * h->num_sms * Sh::ROWS * Sh::DV);
+  return w;
+}
+int heads_tile_of(const mlra_ctx* h) { return h->heads_block < h->np ? h->heads_block : h->np; }
+
+// Whether a prompt call of these sizes takes the per-head form (unless its query is fp32): form every
+// head's keys and values of the cached rows once, then attend with keys of d_h + d_rope and values
+// of d_h. Against the absorbed form it saves MMA work where d_b > d_h (640 against 1152 FLOPs a
+// query, key and head at d_b = 256, 2176 at 512) and the two projections' query-sided traffic, and
+// costs 512 bytes a cached token and head: worth it where the cached rows are few against the query
+// tokens. Their number is known on the device only; the host goes by the table's capacity.
+bool per_head_sizes(const mlra_ctx* h, int total_q, int batch, int pt_stride) {
+  if (h->summed || h->fp8 || h->var == kTiny) return false;
+  const long long rows = (long long)batch * pt_stride * kPage;
+  return rows <= 4LL * total_q && rows * h->cfg.h <= 0x7fffffffLL - 128;
 }
 
 struct PrefillWorkspace {
@@ -143,10 +169,37 @@ PrefillWorkspace carve_prefill(const mlra_ctx* h, int total_q, int batch, int pt
   w.status = c.take<int>(64);
   w.q_pack = c.take<__nv_bfloat16>((size_t)total_q * h->nsub * h->np * (h->d_b + h->d_r));
   w.o = c.take<__nv_bfloat16>((size_t)total_q * h->vh * h->d_b);
-  w.rows = carve_rows(h, c, total_q, batch, false);
+  w.rows = with_rows(h->var, [&](auto sh) {
+    return carve_rows<decltype(sh)>(h, c, total_q, batch, heads_tile_of(h), false);
+  });
   w.pages = h->fp8 ? c.take<__nv_bfloat16>((size_t)batch * pt_stride * kPage * (h->cfg.d_c + h->d_r)) : nullptr;
   w.bytes = c.off;
   return w;
+}
+
+struct HeadWorkspace {
+  int* status;
+  __nv_bfloat16* kv;   // [h][rows][2 * d_h]
+  __nv_bfloat16* kr;   // [rows][d_rope]
+  RowsWorkspace rows;
+  size_t bytes;
+};
+HeadWorkspace carve_head(const mlra_ctx* h, int total_q, int batch, int pt_stride, void* base) {
+  Carver c = {static_cast<char*>(base), 0};
+  const size_t rows = (size_t)batch * pt_stride * kPage;
+  HeadWorkspace w;
+  w.status = c.take<int>(64);
+  w.kv = c.take<__nv_bfloat16>(rows * h->cfg.h * 2 * h->cfg.d_h);
+  w.kr = c.take<__nv_bfloat16>(rows * h->d_r);
+  w.rows = carve_rows<RowsHead>(h, c, total_q, batch, 1, false);
+  w.bytes = c.off;
+  return w;
+}
+size_t prefill_bytes(const mlra_ctx* h, int total_q, int batch, int pt_stride) {
+  const size_t a = carve_prefill(h, total_q, batch, pt_stride, nullptr).bytes;
+  if (!per_head_sizes(h, total_q, batch, pt_stride)) return a;
+  const size_t b = carve_head(h, total_q, batch, pt_stride, nullptr).bytes;
+  return a > b ? a : b;  // (an fp32 query takes the absorbed form)
 }
 
 struct PrefixWorkspace {
@@ -162,18 +215,21 @@ PrefixWorkspace carve_prefix(const mlra_ctx* h, int batch, int groups, void* bas
   Carver c = {static_cast<char*>(base), w.dec.bytes};
   w.o = c.take<float>((size_t)batch * h->vh * h->d_b);
   w.lse = c.take<float>((size_t)batch * h->vh);
-  w.rows = carve_rows(h, c, batch, groups, true);
+  w.rows = with_rows(h->var, [&](auto sh) {
+    return carve_rows<decltype(sh)>(h, c, batch, groups, heads_tile_of(h), true);
+  });
   w.bytes = c.off;
   return w;
 }
 
-bool make_qpack_map(CUtensorMap* m, const mlra_ctx* h, const void* q_pack, uint64_t tokens, uint32_t box_cols,
-                    uint32_t heads, uint32_t box_tokens) {
+// bf16 query rows [tokens][nsub][np][width]; a box is box_cols of `heads` rows of box_tokens tokens.
+bool make_rows_map(CUtensorMap* m, const void* q_pack, uint64_t width, uint64_t np, uint64_t nsub, uint64_t tokens,
+                   uint32_t box_cols, uint32_t heads, uint32_t box_tokens) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return false;
-  const uint64_t row = (uint64_t)(h->d_b + h->d_r) * 2;
-  cuuint64_t dims[4] = {(cuuint64_t)(h->d_b + h->d_r), (cuuint64_t)h->np, (cuuint64_t)h->nsub, tokens};
-  cuuint64_t strides[3] = {row, row * h->np, row * h->np * h->nsub};
+  const uint64_t row = width * 2;
+  cuuint64_t dims[4] = {width, np, nsub, tokens};
+  cuuint64_t strides[3] = {row, row * np, row * np * nsub};
   cuuint32_t box[4] = {box_cols, heads, 1, box_tokens};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q_pack), dims, strides, box, estr,
@@ -191,12 +247,14 @@ struct RowsCall {
   int num_pages;
   const int* page_table;     // null: identity (see RowParams)
   int pt_stride;
+  const __nv_bfloat16* kv;   // per-head form: keys and values, RoPE columns
+  const __nv_bfloat16* kr;
   bool causal;
   RowParams rp;              // results, status (the rest is filled in here)
 };
 
+template <class Sh>
 cudaError_t launch_plan(const mlra_ctx* h, const RowsCall& c, int* status, cudaStream_t s) {
-  const int heads = h->heads_block < h->np ? h->heads_block : h->np;
   RowPlanParams p = {};
   p.cu = c.cu;
   p.lens = c.lens;
@@ -206,71 +264,86 @@ cudaError_t launch_plan(const mlra_ctx* h, const RowsCall& c, int* status, cudaS
   p.causal = c.causal;
   p.plan = c.rp.plan;
   p.status = status;
-  with_rows(h->var, [&](auto sh) {
-    using Sh = decltype(sh);
-    p.tile_tokens = Sh::NQ * (128 / heads);
-    p.key_tile = Sh::KT;
-    p.units = h->nsub * Sh::HALVES;
-    return 0;
-  });
+  p.tile_tokens = Sh::NQ * (128 / (Sh::SPLIT ? 1 : heads_tile_of(h)));
+  p.key_tile = Sh::KT;
+  p.units = Sh::SPLIT ? h->cfg.h : h->nsub * Sh::HALVES;
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = launch_cfg(dim3(1), dim3(kPlanThreads), 0, s, true, &attr);
   return cudaLaunchKernelEx(&cfg, mlra_rows_plan_kernel, p);
 }
 
+template <class Sh>
 cudaError_t launch_rows(const mlra_ctx* h, const RowsCall& c, cudaStream_t s) {
-  return with_rows(h->var, [&](auto sh) {
-    using Sh = decltype(sh);
-    const uint64_t D = h->cfg.d_c + h->d_r;
-    RowParams p = c.rp;
-    p.page_table = c.page_table;
-    p.pt_stride = c.pt_stride;
-    p.num_pages = c.num_pages;
-    p.causal = c.causal;
-    p.nsub = h->nsub;
-    p.chunks = h->chunks;
-    p.heads_tile = h->heads_block < h->np ? h->heads_block : h->np;
-    p.tok_tile = 128 / p.heads_tile;
-    p.heads_block = h->heads_block;
-    p.vh = h->vh;
-    p.d_c = h->cfg.d_c;
-    CUtensorMap mc, mr, mqc, mqr;
-    if (!make_map(&mc, c.pool, (uint64_t)c.num_pages * kPage, D, D * 2, kPage, Sh::CW) ||
-        !make_map(&mr, c.pool, (uint64_t)c.num_pages * kPage, D, D * 2, kPage, Sh::RW) ||
-        !make_qpack_map(&mqc, h, c.q_pack, c.tokens, Sh::CW, p.heads_tile, p.tok_tile) ||
-        !make_qpack_map(&mqr, h, c.q_pack, c.tokens, Sh::RW, p.heads_tile, p.tok_tile))
+  const uint64_t D = h->cfg.d_c + h->d_r;
+  RowParams p = c.rp;
+  p.page_table = c.page_table;
+  p.pt_stride = c.pt_stride;
+  p.num_pages = c.num_pages;
+  p.causal = c.causal;
+  p.nsub = Sh::SPLIT ? h->cfg.h : h->nsub;
+  p.chunks = Sh::SPLIT ? 1 : h->chunks;
+  p.heads_tile = Sh::SPLIT ? 1 : heads_tile_of(h);
+  p.tok_tile = 128 / p.heads_tile;
+  p.heads_block = Sh::SPLIT ? 1 : h->heads_block;
+  p.vh = h->vh;
+  p.d_c = h->cfg.d_c;
+  CUtensorMap mc, mr, mqc, mqr;
+  if (Sh::SPLIT) {
+    // keys and values of a head: rows of 2 * d_h; the queries as they came
+    const uint64_t rows = (uint64_t)c.seqs * c.pt_stride * kPage, w = Sh::DB + Sh::DV;
+    p.kv_rows = (int)rows;
+    if (!make_map(&mc, c.kv, rows * h->cfg.h, w, w * 2, Sh::KT, Sh::CW) ||
+        !make_map(&mr, c.kr, rows, h->d_r, (uint64_t)h->d_r * 2, Sh::KT, Sh::RW) ||
+        !make_rows_map(&mqc, c.q_pack, h->cfg.d_h + h->d_r, 1, h->cfg.h, c.tokens, Sh::CW, 1, 128) ||
+        !make_rows_map(&mqr, c.q_pack, h->cfg.d_h + h->d_r, 1, h->cfg.h, c.tokens, Sh::RW, 1, 128))
       return cudaErrorInvalidValue;
-    cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = launch_cfg(dim3(h->num_sms), dim3(Sh::THREADS), Sh::SMEM, s, true, &attr);
-    return cudaLaunchKernelEx(&cfg, mlra_rows_kernel<Sh>, mc, mr, mqc, mqr, p);
-  });
+  } else if (!make_map(&mc, c.pool, (uint64_t)c.num_pages * kPage, D, D * 2, kPage, Sh::CW) ||
+             !make_map(&mr, c.pool, (uint64_t)c.num_pages * kPage, D, D * 2, kPage, Sh::RW) ||
+             !make_rows_map(&mqc, c.q_pack, h->d_b + h->d_r, h->np, h->nsub, c.tokens, Sh::CW, p.heads_tile, p.tok_tile) ||
+             !make_rows_map(&mqr, c.q_pack, h->d_b + h->d_r, h->np, h->nsub, c.tokens, Sh::RW, p.heads_tile, p.tok_tile)) {
+    return cudaErrorInvalidValue;
+  }
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = launch_cfg(dim3(h->num_sms), dim3(Sh::THREADS), Sh::SMEM, s, true, &attr);
+  return cudaLaunchKernelEx(&cfg, mlra_rows_kernel<Sh>, mc, mr, mqc, mqr, p);
 }
 
+template <class Sh>
 cudaError_t launch_merge(const mlra_ctx* h, const RowsCall& c, cudaStream_t s) {
-  return with_rows(h->var, [&](auto sh) {
-    using Sh = decltype(sh);
-    MergeParams m = {};
-    m.plan = c.rp.plan;
-    m.ctas = h->num_sms;
-    m.causal = c.causal;
-    m.key_tile = Sh::KT;
-    m.halves = Sh::HALVES;
-    m.chunks = h->chunks;
-    m.heads_tile = h->heads_block < h->np ? h->heads_block : h->np;
-    m.tok_tile = 128 / m.heads_tile;
-    m.heads_block = h->heads_block;
-    m.vh = h->vh;
-    m.db = Sh::DB;
-    m.dv = Sh::DV;
-    m.rows = Sh::ROWS;
-    m.part_o = c.rp.part_o;
-    m.part_lse = c.rp.part_lse;
-    m.o_bf16 = c.rp.o_bf16;
-    m.lse = c.rp.lse;
-    cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = launch_cfg(dim3(h->num_sms, Sh::ROWS / 8), dim3(256), 0, s, true, &attr);
-    return cudaLaunchKernelEx(&cfg, mlra_rows_merge_kernel, m);
-  });
+  MergeParams m = {};
+  m.plan = c.rp.plan;
+  m.causal = c.causal;
+  m.key_tile = Sh::KT;
+  m.halves = Sh::HALVES;
+  m.chunks = Sh::SPLIT ? 1 : h->chunks;
+  m.heads_tile = Sh::SPLIT ? 1 : heads_tile_of(h);
+  m.tok_tile = 128 / m.heads_tile;
+  m.heads_block = Sh::SPLIT ? 1 : h->heads_block;
+  m.vh = h->vh;
+  m.db = Sh::DB;
+  m.dv = Sh::DV;
+  m.rows = Sh::ROWS;
+  m.part_o = c.rp.part_o;
+  m.part_lse = c.rp.part_lse;
+  m.o_bf16 = c.rp.o_bf16;
+  m.o_f32 = c.rp.o_f32;
+  m.lse = c.rp.lse;
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = launch_cfg(dim3(h->num_sms, Sh::ROWS / 8), dim3(256), 0, s, true, &attr);
+  return cudaLaunchKernelEx(&cfg, mlra_rows_merge_kernel, m);
+}
+
+// Keys and values of every head for the per-head form.
+template <int DBB>
+cudaError_t launch_expand(const mlra_ctx* h, const UpParams& up, cudaStream_t s) {
+  using Sh = UpShape<DBB, 128, 1>;
+  CUtensorMap mc;
+  const uint64_t D = h->cfg.d_c + h->d_r;
+  if (!make_map(&mc, up.pool, (uint64_t)up.num_pages * kPage, D, D * 2, kPage, Sh::CW)) return cudaErrorInvalidValue;
+  const int per_sm = 2 * (Sh::SMEM + 1024) <= 227 * 1024 ? 2 : 1;
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = launch_cfg(dim3(h->num_sms * per_sm), dim3(Sh::THREADS), Sh::SMEM, s, true, &attr);
+  return cudaLaunchKernelEx(&cfg, mlra_rows_up_kernel<Sh, true>, h->map_wuk, h->map_wuv, mc, up);
 }
 
 template <int DBB, int DH, int SUMK>
@@ -293,7 +366,7 @@ cudaError_t launch_up(const mlra_ctx* h, const __nv_bfloat16* o, int tokens, con
   const int grid = (int)(items < (long long)h->num_sms * per_sm ? items : (long long)h->num_sms * per_sm);
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = launch_cfg(dim3(grid), dim3(Sh::THREADS), Sh::SMEM, s, true, &attr);
-  return cudaLaunchKernelEx(&cfg, mlra_rows_up_kernel<Sh>, h->map_wuv, mo, up);
+  return cudaLaunchKernelEx(&cfg, mlra_rows_up_kernel<Sh>, h->map_wuv, h->map_wuv, mo, up);
 }
 
 // bf16 absorb for every variant (the E4M3 cache's scales go into the two query scales)
@@ -335,6 +408,61 @@ bool rows_sizes_ok(int total_q, int batch, int pt_stride) {
          (long long)pt_stride * kPage <= 0x7fffffffLL - kTile;
 }
 
+// The per-head form (see per_head_sizes): expansion, plan, attention, merge.
+int run_prefill_heads(mlra_handle h, const void* q, const int32_t* cu, int total_q, const void* pool, int num_pages,
+                      const int32_t* page_table, int pt_stride, const int32_t* seq_lens, int batch, void* out,
+                      mlra_dtype out_dtype, float* lse, void* workspace, cudaStream_t s) {
+  const HeadWorkspace w = carve_head(h, total_q, batch, pt_stride, workspace);
+  const EarlyTags tags = {reinterpret_cast<unsigned*>(w.status) + 1, next_call_tag()};
+  UpParams up = {};
+  up.heads = h->cfg.h;
+  up.status = w.status;
+  up.wait_limit_ns = kWaitLimitNs;
+  up.tags = tags;
+  up.lens = seq_lens;
+  up.page_table = page_table;
+  up.pt_stride = pt_stride;
+  up.batch = batch;
+  up.num_pages = num_pages;
+  up.heads_block = h->heads_block;
+  up.kv_rows = batch * pt_stride * kPage;
+  up.width = h->cfg.d_c + h->d_r;
+  up.d_c = h->cfg.d_c;
+  up.d_r = h->d_r;
+  up.pool = static_cast<const __nv_bfloat16*>(pool);
+  up.kv = w.kv;
+  up.kr = w.kr;
+  RowsCall c = {};
+  c.q_pack = static_cast<const __nv_bfloat16*>(q);
+  c.tokens = total_q;
+  c.seqs = batch;
+  c.cu = cu;
+  c.lens = seq_lens;
+  c.pt_stride = pt_stride;
+  c.kv = w.kv;
+  c.kr = w.kr;
+  c.causal = true;
+  c.rp.plan = w.rows.plan;
+  c.rp.s_scale = h->scale * kLog2e;
+  c.rp.o_scale = 1.f;
+  c.rp.o_bf16 = out_dtype == MLRA_BF16 ? static_cast<__nv_bfloat16*>(out) : nullptr;
+  c.rp.o_f32 = out_dtype == MLRA_F32 ? static_cast<float*>(out) : nullptr;
+  c.rp.lse = lse;
+  c.rp.lse_mul = kLn2;
+  c.rp.part_o = w.rows.part_o;
+  c.rp.part_lse = w.rows.part_lse;
+  c.rp.status = w.status;
+  c.rp.tags = tags;
+  c.rp.wait_limit_ns = kWaitLimitNs;
+  g_use_pdl = true;
+  cudaError_t e = h->d_b == 128 ? launch_expand<128>(h, up, s)
+                : h->d_b == 256 ? launch_expand<256>(h, up, s) : launch_expand<512>(h, up, s);
+  if (e == cudaSuccess) e = launch_plan<RowsHead>(h, c, w.status, s);
+  if (e == cudaSuccess) e = launch_rows<RowsHead>(h, c, s);
+  if (e == cudaSuccess) e = launch_merge<RowsHead>(h, c, s);
+  return e == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
+}
+
 int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t* cu, int total_q, const void* pool,
                 int num_pages, const int32_t* page_table, int pt_stride, const int32_t* seq_lens, int batch, void* out,
                 mlra_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
@@ -348,14 +476,15 @@ int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t*
   if ((long long)num_pages * kPage > 0x7fffffffLL ||
       (h->fp8 && (long long)batch * pt_stride * kPage > 0x7fffffffLL))
     return MLRA_ERR_UNSUPPORTED;
-  PrefillWorkspace w = carve_prefill(h, total_q, batch, pt_stride, workspace);
-  if (ws_bytes < w.bytes) return MLRA_ERR_WORKSPACE;
+  if (ws_bytes < prefill_bytes(h, total_q, batch, pt_stride)) return MLRA_ERR_WORKSPACE;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev != h->device) return MLRA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (total_q == 0)
-    return cudaMemsetAsync(w.status, 0, 4, s) == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
-
+  if (total_q == 0) return cudaMemsetAsync(workspace, 0, 4, s) == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
+  if (q_dtype == MLRA_BF16 && per_head_sizes(h, total_q, batch, pt_stride))
+    return run_prefill_heads(h, q, cu, total_q, pool, num_pages, page_table, pt_stride, seq_lens, batch, out, out_dtype,
+                             lse, workspace, s);
+  PrefillWorkspace w = carve_prefill(h, total_q, batch, pt_stride, workspace);
   const EarlyTags tags = {reinterpret_cast<unsigned*>(w.status) + 1, next_call_tag()};
   ProjParams pp = absorb_params(h, q, q_dtype, total_q, w.q_pack, w.status, tags);
   // The scores are scaled in the softmax, so that q^R goes in as it is (a bf16 query's is not
@@ -378,6 +507,7 @@ int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t*
   c.rp.o_scale = h->fp8 ? h->latent_scale : 1.f;
   c.rp.o_bf16 = w.o;
   c.rp.lse = lse;
+  c.rp.lse_mul = kLn2;
   c.rp.part_o = w.rows.part_o;
   c.rp.part_lse = w.rows.part_lse;
   c.rp.status = w.status;
@@ -392,12 +522,22 @@ int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t*
     e = cudaLaunchKernelEx(&cfg, mlra_widen_pages_kernel, static_cast<const uint8_t*>(pool), num_pages, page_table,
                            pt_stride, seq_lens, h->cfg.d_c + h->d_r, w.pages, w.status);
   }
-  if (e == cudaSuccess) e = launch_plan(h, c, w.status, s);
-  if (e == cudaSuccess) e = launch_rows(h, c, s);
-  if (e == cudaSuccess) e = launch_merge(h, c, s);
+  if (e == cudaSuccess)
+    e = with_rows(h->var, [&](auto sh) {
+      using Sh = decltype(sh);
+      cudaError_t r = launch_plan<Sh>(h, c, w.status, s);
+      if (r == cudaSuccess) r = launch_rows<Sh>(h, c, s);
+      return r == cudaSuccess ? launch_merge<Sh>(h, c, s) : r;
+    });
   if (e == cudaSuccess) {
-    const UpParams up = {w.rows.plan.hdr + 1, out, out_dtype == MLRA_F32, h->cfg.h, h->summed ? h->alpha : 1.f,
-                         w.status, kWaitLimitNs};
+    UpParams up = {};
+    up.used = w.rows.plan.hdr + 1;
+    up.out = out;
+    up.out_f32 = out_dtype == MLRA_F32;
+    up.heads = h->cfg.h;
+    up.out_scale = h->summed ? h->alpha : 1.f;
+    up.status = w.status;
+    up.wait_limit_ns = kWaitLimitNs;
     switch (h->var) {
       case kTiny: e = h->summed ? launch_up<32, 32, 4>(h, w.o, total_q, up, s) : launch_up<32, 32, 1>(h, w.o, total_q, up, s); break;
       case kMlra2: e = launch_up<256, 128, 1>(h, w.o, total_q, up, s); break;
@@ -459,6 +599,7 @@ int run_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const vo
   c.rp.o_scale = 1.f;
   c.rp.o_f32 = w.o;
   c.rp.lse = w.lse;
+  c.rp.lse_mul = 1.f;
   c.rp.part_o = w.rows.part_o;
   c.rp.part_lse = w.rows.part_lse;
   c.rp.status = w.dec.status;
@@ -517,7 +658,8 @@ int run_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const vo
 
   g_use_pdl = true;
   cudaError_t e = dispatch_absorb_rows(h, pp, batch, s);
-  if (e == cudaSuccess) e = launch_plan(h, c, w.dec.status, s);
+  if (e == cudaSuccess)
+    e = with_rows(h->var, [&](auto sh) { return launch_plan<decltype(sh)>(h, c, w.dec.status, s); });
   if (e == cudaSuccess) switch (h->var) {
       case kTiny: e = launch_decode<DecTiny>(h, mc, mr, mqc, mqr, dp, s); break;
       case kMlra4: e = launch_decode<DecMlra4>(h, mc, mr, mqc, mqr, dp, s); break;
@@ -525,7 +667,7 @@ int run_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const vo
       case kMla: e = launch_decode<DecMla>(h, mc, mr, mqc, mqr, dp, s); break;
       default: e = launch_decode<DecMlra2>(h, mc, mr, mqc, mqr, dp, s); break;
     }
-  if (e == cudaSuccess) e = launch_rows(h, c, s);
+  if (e == cudaSuccess) e = with_rows(h->var, [&](auto sh) { return launch_rows<decltype(sh)>(h, c, s); });
   if (e == cudaSuccess) switch (h->var) {
       case kTiny:
         e = h->summed ? dispatch_uproj_prefix<128, 32, 4>(h, pp, batch, s) : dispatch_uproj_prefix<32, 32, 1>(h, pp, batch, s);
