@@ -109,7 +109,8 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // queue is full, and each wait costs a few hundred clocks, which one warp's MMAs hide for the other.
 // VST > 0: the per-head form. Keys and values are two buffers (a head's own, formed by the expansion
 // kernel), so values have a ring of VST places of their own, and a tile's keys and RoPE columns are
-// done with as soon as its scores are formed. A row tile is then 128 tokens of one head.
+// done with as soon as its scores are formed. A row tile is then 128 tokens of one head. The values
+// are finite (see the expansion), so no tile is patched.
 template <int DB_, int DR_, int KT_, int DV_, int NQ_, int CST_, int RST_, int VST_ = 0>
 struct RowShape {
   static constexpr int DB = DB_, DR = DR_, KT = KT_, DV = DV_, NQ = NQ_, CST = CST_, RST = RST_,
@@ -169,7 +170,7 @@ struct RowParams {
   int d_c;
   float s_scale;           // from a score (packed query times staged row) to log2 units
   float o_scale;           // value of a staged latent element (1, or the E4M3 cache's scale)
-  int kv_rows;             // per-head form: rows of a head's key / value buffer (pt_stride pages a sequence)
+  int seq_rows, kv_rows;   // per-head form: rows a sequence and a head have in the key / value buffer
   __nv_bfloat16* o_bf16;   // [tokens][vh][DB], or null
   float* o_f32;            // [tokens][vh][DB] when o_bf16 is null
   float* lse;              // [tokens][vh] or null
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         const int nrow = rows_of(u);
         if constexpr (SPLIT) {
           // keys a tile ahead of values, whose place comes free later
-          const int r0 = u.t.b * p.pt_stride * kPage, y0 = sub * p.kv_rows + r0;
+          const int r0 = u.t.b * p.seq_rows, y0 = sub * p.kv_rows + r0;
           if (lane == 0) {
             auto load_keys = [&](int t, uint32_t n) {
               const int s = n % CST;
@@ -384,8 +385,6 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
               for (int r = 0; r < DV / Sh::CW; ++r)
                 tma_load_2d(vring + s * Sh::V_BYTES + r * Sh::KC_REG, &map_c, &vfull[s], Sh::DB + r * Sh::CW,
                             y0 + t * KT, pol);
-              // (the patch warp may look at this phase of vfull only now)
-              if ((t + 1) * KT > u.t.lim0) mbar_arrive(&patch[s]);
             }
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -541,7 +540,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
             if (q >= nrow || !ok) break;
             ok = wait(&pfull[q], pc[q] & 1);
             ++pc[q];
-            if (q == 0 && (u.begin + i + 1) * KT > u.t.lim0) {
+            if (!SPLIT && q == 0 && (u.begin + i + 1) * KT > u.t.lim0) {
               ok = ok && wait(&patched[kt % PST], (fixes >> (kt % PST)) & 1);
               fixes ^= 1u << (kt % PST);
             }
@@ -615,33 +614,46 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         if (!ok) break;
         const int lim = tile_limit(u.t, p.causal);
         for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
-          if ((t + 1) * KT <= u.t.lim0) continue;
-          // the MMAs that form this key tile's scores have read it (and it had landed); per-head form:
-          // its values have been asked for, and land
-          ok = wait(&patch[kt % PST], (fixes >> (kt % PST)) & 1) &&
-               (SPLIT ? wait(&vfull[kt % PST], (kt / PST) & 1) : wait(&kfull[kt % PST], (kt / PST) & 1));
+          if (SPLIT || (t + 1) * KT <= u.t.lim0) continue;
+          // the MMAs that form this key tile's scores have read it (and it had landed)
+          ok = wait(&patch[kt % PST], (fixes >> (kt % PST)) & 1) && wait(&kfull[kt % PST], (kt / PST) & 1);
           if (!ok) break;
           fixes ^= 1u << (kt % PST);
-          uint8_t* st_mem = vring + (kt % PST) * (SPLIT ? Sh::V_BYTES : Sh::C_BYTES);
+          uint8_t* st_mem = cring + (kt % PST) * Sh::C_BYTES;
           const int k0 = t * KT;
           const int some = max(0, min(KT, max(u.t.lim0, 0) - k0));  // rows [some, none) only some tokens see
           const int none = max(0, min(KT, lim - k0));
-          constexpr int CPR = Sh::C_ROWB / 16;
-          for (int r = 0; r < (SPLIT ? DV / Sh::CW : Sh::NC); ++r) {
-            uint8_t* reg = st_mem + r * Sh::KC_REG;
+          constexpr int CPR = Sh::C_ROWB / 16, REGS = Sh::NC;
+          for (int r = 0; r < REGS; ++r)
+#pragma unroll 4
             for (int i = none * CPR + lane; i < KT * CPR; i += 32)
-              *reinterpret_cast<uint4*>(reg + i * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(st_mem + r * Sh::KC_REG + i * 16) = make_uint4(0, 0, 0, 0);
+          // 0 x value sums to NaN where any is not finite (rare): one multiply-add a pair, and eight
+          // loads under way, for up to 32 KB
+          const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+          __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
+          for (int r = 0; r < REGS; ++r)
+#pragma unroll 8
             for (int i = some * CPR + lane; i < none * CPR; i += 32) {
-              uint4 x = *reinterpret_cast<const uint4*>(reg + i * 16);
-              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-              bool hit = false;
+              const uint4 x = *reinterpret_cast<const uint4*>(st_mem + r * Sh::KC_REG + i * 16);
+              const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&x);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; hit = true; }
-                if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0x0000ffffu; hit = true; }
-              }
-              if (hit) *reinterpret_cast<uint4*>(reg + i * 16) = x;
+              for (int e = 0; e < 4; ++e) acc[e] = __hfma2(h2[e], zero, acc[e]);
             }
+          const float2 bad = __bfloat1622float2(__hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3])));
+          if (__any_sync(0xffffffffu, bad.x != 0.f || bad.y != 0.f)) {  // NaN != 0
+            for (int r = 0; r < REGS; ++r)
+              for (int i = some * CPR + lane; i < none * CPR; i += 32) {
+                uint4* at = reinterpret_cast<uint4*>(st_mem + r * Sh::KC_REG + i * 16);
+                uint4 x = *at;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+                  if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu;
+                }
+                *at = x;
+              }
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -944,9 +956,13 @@ struct UpShape {
 };
 
 // EXPAND: the same product over cached rows instead, for the per-head form: each head's keys c_j W^UK_h
-// and values c_j W^UV_h of every cached token, [head][row][K | V], row = b * pt_stride * page + token; a
-// weight is then one of a head's two. Reads the rows once a weight (from L2 after the first),
-// writes 512 bytes a token and head. The blocks also copy the RoPE columns to rows of their own.
+// and values c_j W^UV_h of every cached token, [head][row][K | V], row = b * seq_rows + token (seq_rows:
+// the table row's pages, rounded up to whole 128-token tiles, all of which are written); a weight is
+// then one of a head's two. Reads the rows once a weight (from L2 after the first), writes 512 bytes
+// a token and head. The blocks also copy the RoPE columns to rows of their own.
+// Values are stored finite, infinities as the largest bf16 value and NaN as 0: a masked key's P = 0
+// then adds nothing. A token that does see a cached row with NaN or infinities gets NaN through the
+// row's keys, which keep them.
 struct UpParams {
   const int* used;       // tokens in use (rows past them are left as they were)
   void* out;             // [tokens][heads][DH]
@@ -958,7 +974,7 @@ struct UpParams {
   EarlyTags tags;
   const int* lens;
   const int* page_table;
-  int pt_stride, batch, num_pages, heads_block, kv_rows, width, d_c, d_r;
+  int pt_stride, batch, num_pages, heads_block, seq_rows, kv_rows, width, d_c, d_r;
   const __nv_bfloat16* pool;
   __nv_bfloat16* kv;     // [heads][kv_rows][2 * DH]
   __nv_bfloat16* kr;     // [kv_rows][d_r]
@@ -1138,7 +1154,8 @@ __global__ void __launch_bounds__(Sh::THREADS)
         if (id < 0 || id >= p.num_pages) id = 0;  // (reported by the loads)
         for (int i = tid; i < kPage * cpr; i += 128) {
           const int r = i / cpr, x = (i % cpr) * 8;
-          *reinterpret_cast<uint4*>(p.kr + ((size_t)pg * kPage + r) * p.d_r + x) = __ldg(
+          const size_t at = (size_t)b * p.seq_rows + (pg - b * p.pt_stride) * kPage + r;
+          *reinterpret_cast<uint4*>(p.kr + at * p.d_r + x) = __ldg(
               reinterpret_cast<const uint4*>(p.pool + ((size_t)id * kPage + r) * p.width + p.d_c + x));
         }
       }
@@ -1158,7 +1175,11 @@ __global__ void __launch_bounds__(Sh::THREADS)
           for (int e = 0; e < 32; ++e) v[e] *= p.out_scale;
         }
         if constexpr (EXPAND) {
-          // the sequence's rows end with its table row, within the tile where that has an odd page
+          if (h & 1) {
+            constexpr float kMax = 3.3895314e38f;  // the largest bf16 value
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = v[e] == v[e] ? fminf(fmaxf(v[e], -kMax), kMax) : 0.f;
+          }
           uint4 v4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -1166,11 +1187,10 @@ __global__ void __launch_bounds__(Sh::THREADS)
                                pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
           exchange4(v4, lane);
           const int b = tile / seq_tiles, t0 = (tile % seq_tiles) * 128 + (row & ~3);
-          __nv_bfloat16* dst = p.kv + ((size_t)(h / 2) * p.kv_rows + (size_t)b * p.pt_stride * kPage + t0) * (2 * DH) +
+          __nv_bfloat16* dst = p.kv + ((size_t)(h / 2) * p.kv_rows + (size_t)b * p.seq_rows + t0) * (2 * DH) +
                                (h & 1) * DH + c + (lane & 3) * 8;
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (t0 + r < p.pt_stride * kPage) *reinterpret_cast<uint4*>(dst + (size_t)r * 2 * DH) = v4[r];
+          for (int r = 0; r < 4; ++r) *reinterpret_cast<uint4*>(dst + (size_t)r * 2 * DH) = v4[r];
         } else if (p.out_f32) {
           // (rows behind the last sequence, tok >= used, stay as they were)
           float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((size_t)tok * p.heads + h) * DH + c);

@@ -143,16 +143,25 @@ RowsWorkspace carve_rows(const mlra_ctx* h, Carver& c, size_t tokens, size_t seq
 }
 int heads_tile_of(const mlra_ctx* h) { return h->heads_block < h->np ? h->heads_block : h->np; }
 
+// Rows of a sequence in the per-head buffers: whole 128-token tiles.
+long long seq_rows_of(int pt_stride) { return ((long long)pt_stride + 1) / 2 * kTile; }
+
 // Whether a prompt call of these sizes takes the per-head form (unless its query is fp32): form every
 // head's keys and values of the cached rows once, then attend with keys of d_h + d_rope and values
 // of d_h. Against the absorbed form it saves MMA work where d_b > d_h (640 against 1152 FLOPs a
 // query, key and head at d_b = 256, 2176 at 512) and the two projections' query-sided traffic, and
 // costs 512 bytes a cached token and head: worth it where the cached rows are few against the query
-// tokens. Their number is known on the device only; the host goes by the table's capacity.
+// tokens. Their number is known on the device only; the host goes by the table's capacity. At
+// d_b = d_h = 128 the MMA work is the same, and every CTA then streams keys and values of its own
+// where the absorbed form's 32 heads share theirs: measured (one prompt, 128 heads) 269 against 288
+// us at 2048 tokens, 807 against 789 at 4096, 11.3 against 9.4 ms at 16384. At d_b = 256: 131 against
+// 239 us at 1024, 846 against 1808 at 4096; at 512: 87 against 249 us at 512, 0.91 against 6.8 ms at
+// 4096.
 bool per_head_sizes(const mlra_ctx* h, int total_q, int batch, int pt_stride) {
   if (h->summed || h->fp8 || h->var == kTiny) return false;
-  const long long rows = (long long)batch * pt_stride * kPage;
-  return rows <= 4LL * total_q && rows * h->cfg.h <= 0x7fffffffLL - 128;
+  const long long rows = (long long)batch * seq_rows_of(pt_stride);  // a row's index is 32 bits
+  return (h->d_b > 128 || pt_stride <= 2048 / kPage) && (long long)batch * pt_stride * kPage <= 4LL * total_q &&
+         rows * h->cfg.h <= 0x7fffffffLL - kTile;
 }
 
 struct PrefillWorkspace {
@@ -186,7 +195,7 @@ struct HeadWorkspace {
 };
 HeadWorkspace carve_head(const mlra_ctx* h, int total_q, int batch, int pt_stride, void* base) {
   Carver c = {static_cast<char*>(base), 0};
-  const size_t rows = (size_t)batch * pt_stride * kPage;
+  const size_t rows = (size_t)batch * seq_rows_of(pt_stride);
   HeadWorkspace w;
   w.status = c.take<int>(64);
   w.kv = c.take<__nv_bfloat16>(rows * h->cfg.h * 2 * h->cfg.d_h);
@@ -290,7 +299,8 @@ cudaError_t launch_rows(const mlra_ctx* h, const RowsCall& c, cudaStream_t s) {
   CUtensorMap mc, mr, mqc, mqr;
   if (Sh::SPLIT) {
     // keys and values of a head: rows of 2 * d_h; the queries as they came
-    const uint64_t rows = (uint64_t)c.seqs * c.pt_stride * kPage, w = Sh::DB + Sh::DV;
+    const uint64_t rows = (uint64_t)c.seqs * seq_rows_of(c.pt_stride), w = Sh::DB + Sh::DV;
+    p.seq_rows = (int)seq_rows_of(c.pt_stride);
     p.kv_rows = (int)rows;
     if (!make_map(&mc, c.kv, rows * h->cfg.h, w, w * 2, Sh::KT, Sh::CW) ||
         !make_map(&mr, c.kr, rows, h->d_r, (uint64_t)h->d_r * 2, Sh::KT, Sh::RW) ||
@@ -425,7 +435,8 @@ int run_prefill_heads(mlra_handle h, const void* q, const int32_t* cu, int total
   up.batch = batch;
   up.num_pages = num_pages;
   up.heads_block = h->heads_block;
-  up.kv_rows = batch * pt_stride * kPage;
+  up.seq_rows = (int)seq_rows_of(pt_stride);
+  up.kv_rows = batch * up.seq_rows;
   up.width = h->cfg.d_c + h->d_r;
   up.d_c = h->cfg.d_c;
   up.d_r = h->d_r;
