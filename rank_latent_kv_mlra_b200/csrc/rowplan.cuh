@@ -22,6 +22,7 @@ struct RowPlan {
                        // [3] token tiles without a key
   long long* start;    // [max tiles + 1] position of each tile's first unit; the last is the total
   TokenTile* tile;     // [max tiles]
+  int* base;           // [batch + 1] first token tile of each sequence
   int* tok_tile;       // [tokens] tile of each token, or null
   int4* cut;           // [2 * CTAs] the unit each CTA's stretch goes on with: first and last CTA, unit;
                        // first token, tokens (written by the attention kernel, for the merge)
@@ -109,6 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const R
   const int tiles = (flags[0] & 2) ? 0 : running;
   if (threadIdx.x == 0) base[p.batch] = running;
   __syncthreads();
+  for (int b = threadIdx.x; b <= p.batch; b += kPlanThreads) p.plan.base[b] = base[b];
   long long pos = 0;
   for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
     const int i = i0 + threadIdx.x;
@@ -181,6 +183,9 @@ struct UnitWalk {
   int i, tiles, units, key_tile, causal;
   TokenTile t;
   int kv;
+  // whole units in turn instead of a stretch (see whole_units): CTA c takes units c, c + step, ... of
+  // an order that goes through a sequence's sub-units one after the other, long units first
+  int unit, step;
   __device__ __forceinline__ void load() {
     at = __ldg(plan->start + i);
     nx = __ldg(plan->start + i + 1);
@@ -208,6 +213,38 @@ struct UnitWalk {
     }
     i = lo;
     if (pos < hi) load();
+  }
+  __device__ __forceinline__ void init_whole(const RowPlan* pl, int tiles_, int cta, int ctas, int units_, int key_tile_,
+                                             int causal_) {
+    plan = pl;
+    tiles = tiles_;
+    units = units_;
+    key_tile = key_tile_;
+    causal = causal_;
+    unit = cta;
+    step = ctas;
+    pos = hi = 0;
+  }
+  __device__ __forceinline__ UnitPart next_whole() {
+    UnitPart u;
+    u.valid = false;
+    u.begin = u.end = u.kv = u.sub = 0;
+    u.t = {0, 0, 0, 0};
+    for (; unit < tiles * units; unit += step) {
+      const int b = __ldg(&plan->tile[unit / units].b);
+      const int first = __ldg(plan->base + b), n = __ldg(plan->base + b + 1) - first;
+      const int r = unit - first * units;  // within the sequence's units
+      i = first + n - 1 - r % n;
+      const int4 raw = __ldg(reinterpret_cast<const int4*>(plan->tile + i));
+      u.t.b = raw.x; u.t.tok0 = raw.y; u.t.ntok = raw.z; u.t.lim0 = raw.w;
+      u.kv = u.end = key_tiles(u.t, causal, key_tile);
+      if (u.kv == 0) continue;
+      u.sub = r / n;
+      u.valid = true;
+      unit += step;
+      return u;
+    }
+    return u;
   }
   __device__ __forceinline__ UnitPart next() {
     UnitPart u;

@@ -135,6 +135,7 @@ RowsWorkspace carve_rows(const mlra_ctx* h, Carver& c, size_t tokens, size_t seq
   w.plan.hdr = c.take<int>(4);
   w.plan.start = c.take<long long>(tiles + 1);
   w.plan.tile = c.take<TokenTile>(tiles);
+  w.plan.base = c.take<int>(seqs + 1);
   w.plan.cut = c.take<int4>((size_t)2 * h->num_sms);
   w.plan.tok_tile = tok_tile ? c.take<int>(tokens) : nullptr;
   w.part_lse = c.take<float>((size_t)2 * h->num_sms * Sh::ROWS);
@@ -151,17 +152,15 @@ long long seq_rows_of(int pt_stride) { return ((long long)pt_stride + 1) / 2 * k
 // of d_h. Against the absorbed form it saves MMA work where d_b > d_h (640 against 1152 FLOPs a
 // query, key and head at d_b = 256, 2176 at 512) and the two projections' query-sided traffic, and
 // costs 512 bytes a cached token and head: worth it where the cached rows are few against the query
-// tokens. Their number is known on the device only; the host goes by the table's capacity. At
-// d_b = d_h = 128 the MMA work is the same, and every CTA then streams keys and values of its own
-// where the absorbed form's 32 heads share theirs: measured (one prompt, 128 heads) 269 against 288
-// us at 2048 tokens, 807 against 789 at 4096, 11.3 against 9.4 ms at 16384. At d_b = 256: 131 against
-// 239 us at 1024, 846 against 1808 at 4096; at 512: 87 against 249 us at 512, 0.91 against 6.8 ms at
-// 4096.
+// tokens. Their number is known on the device only; the host goes by the table's capacity.
+// Measured, one prompt of 128 heads, against the absorbed form: d_b = 128: 243 and 288 us at 2048
+// tokens, 753 and 789 at 4096, 9.46 and 9.40 ms at 16384 (24 ragged prompts up to 2047 tokens: 2.21
+// and 2.53 ms); d_b = 256: 0.78 and 1.81 ms at 4096; d_b = 512: 82 and 249 us at 512, 0.84 and 6.8 ms
+// at 4096.
 bool per_head_sizes(const mlra_ctx* h, int total_q, int batch, int pt_stride) {
   if (h->summed || h->fp8 || h->var == kTiny) return false;
   const long long rows = (long long)batch * seq_rows_of(pt_stride);  // a row's index is 32 bits
-  return (h->d_b > 128 || pt_stride <= 2048 / kPage) && (long long)batch * pt_stride * kPage <= 4LL * total_q &&
-         rows * h->cfg.h <= 0x7fffffffLL - kTile;
+  return (long long)batch * pt_stride * kPage <= 4LL * total_q && rows * h->cfg.h <= 0x7fffffffLL - kTile;
 }
 
 struct PrefillWorkspace {

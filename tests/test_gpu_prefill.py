@@ -53,7 +53,7 @@ def make(w, n_q, past, seed=0, q_dtype=torch.bfloat16, behind=0, form=None):
         if table.shape[1] < wide:
             inp["page_table"] = torch.nn.functional.pad(table, (0, wide - table.shape[1]), value=-1).contiguous()
     if form == "heads":
-        assert len(n_q) * table.shape[1] * 64 <= 4 * q.shape[0] and table.shape[1] <= 32
+        assert len(n_q) * table.shape[1] * 64 <= 4 * q.shape[0]
     return w, inp
 
 
