@@ -339,23 +339,37 @@ def mlra_project_append(handle: Handle, x, w_down, positions, pool, page_table, 
     return workspace
 
 
-def _on_one_device(**tensors):
-    """The device all of these tensors (None allowed) are on."""
-    devs = {t.device for t in tensors.values() if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"{', '.join(tensors)} must be on one device")
-    return devs.pop()
+def _one_device(names, *tensors):
+    """The device all of these tensors (None allowed behind the first) are on."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{names} must be on one device")
+    return dev
 
 
-def _workspace(workspace, size: int, device, stream):
-    """The caller's workspace, or one of `size` bytes that outlives the work on `stream`."""
-    if workspace is not None:
-        _require(workspace, "workspace")
-        return workspace
-    workspace = torch.empty(size, dtype=torch.uint8, device=device)
+def _call(name, dev, stream, *args):
+    """Calls the library's `name` on `dev`, with the stream (None: the device's current one) last."""
+    fn = getattr(load_library(), name)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, raw)
+    _check(rc, name)
+
+
+def _new_workspace(size: int, dev, stream):
+    """A workspace of `size` bytes that outlives the work on `stream`."""
+    workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     if stream is not None:
         workspace.record_stream(stream)
     return workspace
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def mlra_prefill_workspace_size(handle: Handle, total_q: int, batch: int, pt_stride: int) -> int:
@@ -404,15 +418,13 @@ def mlra_prefill(handle: Handle, q, cu_seqlens, pool, page_table, seq_lens, out,
     B = page_table.shape[0]
     if cu_seqlens.shape != (B + 1,):
         raise ValueError("cu_seqlens must be [batch + 1]")
-    dev = _on_one_device(q=q, cu_seqlens=cu_seqlens, pool=pool, page_table=page_table, seq_lens=seq_lens, out=out,
-                         lse=lse, workspace=workspace)
-    with torch.cuda.device(dev):
-        workspace = _workspace(workspace, 0 if workspace is not None else
-                               mlra_prefill_workspace_size(handle, total, B, page_table.shape[1]), dev, stream)
-        _check(load_library().mlra_prefill(
-            handle.ptr, _ptr(q), _dtype(q), _ptr(cu_seqlens), total, _ptr(pool), pool.shape[0], _ptr(page_table),
-            page_table.shape[1], _ptr(seq_lens), B, _ptr(out), _dtype(out), _ptr(lse), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(stream)), "mlra_prefill")
+    if workspace is None:
+        workspace = _new_workspace(mlra_prefill_workspace_size(handle, total, B, page_table.shape[1]), q.device, stream)
+    _require(workspace, "workspace")
+    dev = _one_device("the tensors of mlra_prefill", q, cu_seqlens, pool, page_table, seq_lens, out, lse, workspace)
+    _call("mlra_prefill", dev, stream, handle.ptr, q.data_ptr(), _dtype(q), cu_seqlens.data_ptr(), total,
+          pool.data_ptr(), pool.shape[0], page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), B,
+          out.data_ptr(), _dtype(out), _addr(lse), workspace.data_ptr(), workspace.nbytes)
     return workspace
 
 
@@ -437,17 +449,15 @@ def mlra_decode_prefix(handle: Handle, q, pool, prefix_table, prefix_lens, group
     G = prefix_table.shape[0]
     if page_table.shape[0] != B or group_offsets.shape != (G + 1,):
         raise ValueError("page_table must be [batch][stride], group_offsets [groups + 1]")
-    dev = _on_one_device(q=q, pool=pool, prefix_table=prefix_table, prefix_lens=prefix_lens,
-                         group_offsets=group_offsets, page_table=page_table, seq_lens=seq_lens, out=out, lse=lse,
-                         workspace=workspace)
-    with torch.cuda.device(dev):
-        workspace = _workspace(workspace, 0 if workspace is not None else
-                               mlra_decode_prefix_workspace_size(handle, B, G), dev, stream)
-        _check(load_library().mlra_decode_prefix(
-            handle.ptr, _ptr(q), _dtype(q), _ptr(pool), pool.shape[0], _ptr(prefix_table), prefix_table.shape[1],
-            _ptr(prefix_lens), _ptr(group_offsets), G, _ptr(page_table), page_table.shape[1], _ptr(seq_lens), B,
-            _ptr(out), _dtype(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _stream(stream)), "mlra_decode_prefix")
+    if workspace is None:
+        workspace = _new_workspace(mlra_decode_prefix_workspace_size(handle, B, G), q.device, stream)
+    _require(workspace, "workspace")
+    dev = _one_device("the tensors of mlra_decode_prefix", q, pool, prefix_table, prefix_lens, group_offsets, page_table,
+                      seq_lens, out, lse, workspace)
+    _call("mlra_decode_prefix", dev, stream, handle.ptr, q.data_ptr(), _dtype(q), pool.data_ptr(), pool.shape[0],
+          prefix_table.data_ptr(), prefix_table.shape[1], prefix_lens.data_ptr(), group_offsets.data_ptr(), G,
+          page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), B, out.data_ptr(), _dtype(out), _addr(lse),
+          workspace.data_ptr(), workspace.nbytes)
     return workspace
 
 
@@ -464,29 +474,26 @@ def _pages_call(name, handle, pool, refs, page_table, seq_lens, requests, worksp
     _tables(page_table, seq_lens, ("page_table", "seq_lens"))
     if refs.dim() != 1:
         raise ValueError("refs must be [num_pages]")
-    named = dict(refs=refs, page_table=page_table, seq_lens=seq_lens, workspace=workspace, pool=pool, used=used)
+    P, (B, stride) = refs.shape[0], page_table.shape
     if pool is not None:
         _require(pool, "pool", _pool_dtype(handle))
         cfg = handle.cfg
-        if tuple(pool.shape) != (refs.shape[0], cfg.page_size, cfg.d_c + cfg.d_rope):
+        if pool.shape != (P, cfg.page_size, cfg.d_c + cfg.d_rope):
             raise ValueError("pool must be [num_pages][page_size][d_c + d_rope]")
     if used is not None:
         _require(used, "used", torch.int32)
-    for key, t in requests:
-        _require(t, key, torch.int32)
-        if t.dim() != 1 or t.shape != requests[0][1].shape:
+    for t in requests:
+        _require(t, "requests", torch.int32)
+        if t.dim() != 1 or t.shape != requests[0].shape:
             raise ValueError("requests must be vectors of one length")
-        named[key] = t
-    dev = _on_one_device(**named)
-    B, n = page_table.shape[0], requests[0][1].shape[0] if requests else 0
-    with torch.cuda.device(dev):
-        workspace = _workspace(workspace, 0 if workspace is not None else
-                               mlra_pages_workspace_size(handle, refs.shape[0], B), dev, stream)
-        args = [handle.ptr] + ([] if pool is None else [_ptr(pool)])
-        args += [_ptr(refs), refs.shape[0], _ptr(page_table), page_table.shape[1], B, _ptr(seq_lens)]
-        args += [_ptr(t) for _, t in requests] + ([n] if requests else [_ptr(used)])
-        args += [_ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)]
-        _check(getattr(load_library(), name)(*args), name)
+    if workspace is None:
+        workspace = _new_workspace(mlra_pages_workspace_size(handle, P, B), refs.device, stream)
+    _require(workspace, "workspace")
+    dev = _one_device(f"the tensors of {name}", refs, page_table, seq_lens, workspace, pool, used, *requests)
+    lead = (handle.ptr,) if pool is None else (handle.ptr, pool.data_ptr())
+    tail = (*(t.data_ptr() for t in requests), requests[0].shape[0]) if requests else (_addr(used),)
+    _call(name, dev, stream, *lead, refs.data_ptr(), P, page_table.data_ptr(), stride, B, seq_lens.data_ptr(), *tail,
+          workspace.data_ptr(), workspace.nbytes)
     return workspace
 
 
@@ -495,26 +502,26 @@ def mlra_reserve_pages(handle: Handle, refs, page_table, seq_lens, seq_ids, new_
     order) and sets seq_lens to that. refs int32 [num_pages] counts the table entries that hold
     each page. Returns the workspace, whose first int32 is the call's status word."""
     return _pages_call("mlra_reserve_pages", handle, None, refs, page_table, seq_lens,
-                       [("seq_ids", seq_ids), ("new_lens", new_lens)], workspace, stream)
+                       (seq_ids, new_lens), workspace, stream)
 
 
 def mlra_fork_pages(handle: Handle, pool, refs, page_table, seq_lens, src_ids, dst_ids, workspace=None, stream=None):
     """Makes each row of dst_ids (empty rows) a copy of the sequence in src_ids: full pages shared,
     the rows of a partly filled last page copied to a new page. Returns the workspace."""
     return _pages_call("mlra_fork_pages", handle, pool, refs, page_table, seq_lens,
-                       [("src_ids", src_ids), ("dst_ids", dst_ids)], workspace, stream)
+                       (src_ids, dst_ids), workspace, stream)
 
 
 def mlra_free_pages(handle: Handle, refs, page_table, seq_lens, seq_ids, workspace=None, stream=None):
     """Empties the rows of seq_ids; pages that no row holds any more are free. Returns the workspace."""
-    return _pages_call("mlra_free_pages", handle, None, refs, page_table, seq_lens, [("seq_ids", seq_ids)], workspace,
+    return _pages_call("mlra_free_pages", handle, None, refs, page_table, seq_lens, (seq_ids,), workspace,
                        stream)
 
 
 def mlra_compact_pages(handle: Handle, pool, refs, page_table, seq_lens, used=None, workspace=None, stream=None):
     """Moves the used pages to the front of the pool and renames them in every row. `used` (int32,
     one element) receives their number. Returns the workspace."""
-    return _pages_call("mlra_compact_pages", handle, pool, refs, page_table, seq_lens, [], workspace, stream, used)
+    return _pages_call("mlra_compact_pages", handle, pool, refs, page_table, seq_lens, (), workspace, stream, used)
 
 
 def mlra_plan(handle: Handle, seq_lens, pt_stride: int, max_segments: int = 4096, stream=None):

@@ -567,23 +567,21 @@ __global__ void __launch_bounds__(kProjThreads, 1)
     int px0[RB], npx[RB], prow[RB];
     if constexpr (PREFIX) {
       const PrefixParts& pp = p.prefix;
-      const long long total = __ldg(pp.plan.start + __ldg(pp.plan.hdr));
-      const long long pquota = total > 0 ? (total + pp.ctas - 1) / pp.ctas : 1;
+      const int4 h1 = __ldg(reinterpret_cast<const int4*>(pp.plan.hdr) + 1);
+      const long long pquota = join64(h1.x, h1.y);
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
         const int bl = r0 + rb, b = n0 + bl;
         px0[rb] = -1;
         npx[rb] = prow[rb] = 0;
-        const int ti = bl < NT && b < p.batch ? __ldg(pp.plan.tok_tile + b) : -1;
-        if (ti < 0) continue;
-        const TokenTile t = pp.plan.tile[ti];
-        const int kv = key_tiles(t, 0, pp.key_tile);
+        const int4 rec = bl < NT && b < p.batch ? __ldg(pp.plan.tok + b) : make_int4(0, 0, 0, 0);
+        const int kv = rec.z;
         if (kv == 0) continue;
         const int blk = vhead / p.heads_block, hb = vhead % p.heads_block;
         const int usub = (blk * pp.chunks + hb / pp.heads_tile) * pp.halves + f0 / pp.dv;
-        const long long first = __ldg(pp.plan.start + ti) + (long long)usub * unit_cost(kv) + kUnitCost;
+        const long long first = join64(rec.x, rec.y) + (long long)usub * unit_cost(kv) + kUnitCost;
         const int x0 = (int)(first / pquota), x1 = (int)((first + kv - 1) / pquota);
-        const int tok = b - t.tok0;
+        const int tok = rec.w;
         prow[rb] = (tok / pp.tok_tile) * 128 + (tok % pp.tok_tile) * pp.heads_tile + hb % pp.heads_tile;
         npx[rb] = x1 - x0 + 1;
         if (x1 > x0) px0[rb] = x0;

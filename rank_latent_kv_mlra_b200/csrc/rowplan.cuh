@@ -19,11 +19,14 @@ struct TokenTile {
 };
 struct RowPlan {
   int* hdr;            // [0] token tiles, [1] tokens in use (cu[batch]), [2] bad lengths found,
-                       // [3] token tiles without a key
+                       // [3] token tiles without a key, [4, 5] length of a stretch, [6, 7] of the line
+  int4* first;         // [3 * CTAs] where each CTA's stretch begins: tile, its key tiles, its begin and
+                       // end on the line; the tile
   long long* start;    // [max tiles + 1] position of each tile's first unit; the last is the total
   TokenTile* tile;     // [max tiles]
   int* base;           // [batch + 1] first token tile of each sequence
-  int* tok_tile;       // [tokens] tile of each token, or null
+  int4* tok;           // [tokens] begin of the token's tile on the line (two words), the tile's key
+                       // tiles (0: none, or no sequence), the token's place in it; or null
   int4* cut;           // [2 * CTAs] the unit each CTA's stretch goes on with: first and last CTA, unit;
                        // first token, tokens (written by the attention kernel, for the merge)
 };
@@ -33,6 +36,7 @@ struct RowPlanParams {
   int batch, total_q, cap_len;
   int tile_tokens, key_tile, units;  // tokens a token tile, keys a key tile, units a token tile
   int causal;
+  int ctas;            // of the attention kernel
   RowPlan plan;
   int* status;
 };
@@ -46,8 +50,25 @@ __device__ __forceinline__ int key_tiles(const TokenTile& t, int causal, int key
 }
 __device__ __forceinline__ int unit_cost(int kv) { return kv > 0 ? kv + kUnitCost : 0; }
 
+// A CTA's stretch of the line of units.
+struct Stretch {
+  long long lo, hi, quota;
+};
+__device__ __forceinline__ Stretch stretch_of(long long total, int cta, int ctas) {
+  Stretch s;
+  s.quota = total > 0 ? (total + ctas - 1) / ctas : 1;
+  s.lo = min((long long)cta * s.quota, total);
+  s.hi = min(s.lo + s.quota, total);
+  return s;
+}
+
+__device__ __forceinline__ long long join64(int lo, int hi) {
+  return (long long)(((unsigned long long)(unsigned)hi << 32) | (unsigned)lo);
+}
+
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxSeqs = 4096;
+constexpr int kPlanStarts = 2048;  // positions kept in shared memory for the search at the end
 
 // Exclusive scan over the block's threads (32 warps at most); scratch holds a value a warp. Every
 // thread must have read the last call's result before the next call writes scratch: the first
@@ -81,6 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const R
   __shared__ long long scratch[32];
   __shared__ int scratch_i[32];
   __shared__ int flags[2];  // bad lengths; tiles without a key
+  __shared__ long long starts[kPlanStarts];
   if (threadIdx.x < 2) flags[threadIdx.x] = 0;
   __syncthreads();
   grid_launch_dependents();
@@ -103,8 +125,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const R
     running += all;
   }
   if (bad) atomicOr(&flags[0], bad);
-  if (p.plan.tok_tile != nullptr)  // tokens of no sequence
-    for (int i = threadIdx.x; i < p.total_q; i += kPlanThreads) p.plan.tok_tile[i] = -1;
+  if (p.plan.tok != nullptr)  // tokens of no sequence
+    for (int i = threadIdx.x; i < p.total_q; i += kPlanThreads) p.plan.tok[i] = make_int4(0, 0, 0, 0);
   __syncthreads();
   // packed offsets that do not ascend leave no work at all
   const int tiles = (flags[0] & 2) ? 0 : running;
@@ -139,8 +161,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const R
     if (i < tiles) {
       p.plan.start[i] = at;
       p.plan.tile[i] = t;
-      if (p.plan.tok_tile != nullptr)
-        for (int j = 0; j < t.ntok; ++j) p.plan.tok_tile[t.tok0 + j] = i;
+      if (i < kPlanStarts) starts[i] = at;
+      if (p.plan.tok != nullptr)
+        for (int j = 0; j < t.ntok; ++j)
+          p.plan.tok[t.tok0 + j] = make_int4((int)at, (int)(at >> 32), key_tiles(t, p.causal, p.key_tile), j);
     }
     pos += all;
   }
@@ -151,21 +175,33 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const R
     p.plan.hdr[0] = tiles;
     p.plan.hdr[1] = (flags[0] & 2) ? 0 : p.cu[p.batch];
     p.plan.hdr[2] = flags[0];
+    const long long quota = stretch_of(pos, 0, p.ctas).quota;
+    p.plan.hdr[4] = (int)quota;
+    p.plan.hdr[5] = (int)(quota >> 32);
+    p.plan.hdr[6] = (int)pos;
+    p.plan.hdr[7] = (int)(pos >> 32);
+    if (tiles < kPlanStarts) starts[tiles] = pos;
+  }
+  __syncthreads();
+  // where each CTA begins, so that it need not search
+  for (int c = threadIdx.x; c < p.ctas; c += kPlanThreads) {
+    const Stretch s = stretch_of(pos, c, p.ctas);
+    if (s.lo >= s.hi) continue;
+    const long long* st = tiles < kPlanStarts ? starts : p.plan.start;
+    int lo = 0, up = tiles;  // the last tile with start <= lo (tiles without work share their start with the next)
+    while (up - lo > 1) {
+      const int mid = (lo + up) >> 1;
+      if (st[mid] <= s.lo) lo = mid;
+      else up = mid;
+    }
+    const TokenTile t = p.plan.tile[lo];
+    const long long at = st[lo], nx = st[lo + 1];
+    p.plan.first[3 * c] = make_int4(lo, key_tiles(t, p.causal, p.key_tile), (int)at, (int)(at >> 32));
+    p.plan.first[3 * c + 1] = make_int4((int)nx, (int)(nx >> 32), 0, 0);
+    p.plan.first[3 * c + 2] = make_int4(t.b, t.tok0, t.ntok, t.lim0);
   }
   grid_dependency_wait();  // the absorb kernel clears the status word
   if (threadIdx.x == 0 && flags[0]) set_status(p.status, kErrSeqLen);
-}
-
-// A CTA's stretch of the line of units.
-struct Stretch {
-  long long lo, hi, quota;
-};
-__device__ __forceinline__ Stretch stretch_of(long long total, int cta, int ctas) {
-  Stretch s;
-  s.quota = total > 0 ? (total + ctas - 1) / ctas : 1;
-  s.lo = min((long long)cta * s.quota, total);
-  s.hi = min(s.lo + s.quota, total);
-  return s;
 }
 
 // One unit's key tiles that lie in a stretch.
@@ -193,8 +229,8 @@ struct UnitWalk {
     t.b = raw.x; t.tok0 = raw.y; t.ntok = raw.z; t.lim0 = raw.w;
     kv = key_tiles(t, causal, key_tile);
   }
-  __device__ __forceinline__ void init(const RowPlan* pl, int tiles_, const Stretch& s, int units_, int key_tile_,
-                                       int causal_) {
+  __device__ __forceinline__ void init(const RowPlan* pl, int tiles_, const Stretch& s, int cta, int units_,
+                                       int key_tile_, int causal_) {
     plan = pl;
     pos = s.lo;
     hi = s.hi;
@@ -202,17 +238,12 @@ struct UnitWalk {
     key_tile = key_tile_;
     causal = causal_;
     tiles = tiles_;
-    // the last tile with start <= pos (tiles without work share their start with the next)
-    int lo = 0, up = tiles;
-    while (up - lo > 1) {
-      const int step = (up - lo + 31) / 32, probe = lo + lane_id() * step;
-      const bool in = probe < up && __ldg(pl->start + probe) <= pos;
-      const int n = max(__popc(__ballot_sync(0xffffffffu, in)), 1);
-      lo += (n - 1) * step;
-      up = min(lo + step, up);
-    }
-    i = lo;
-    if (pos < hi) load();
+    const int4 a = __ldg(pl->first + 3 * cta), b = __ldg(pl->first + 3 * cta + 1), raw = __ldg(pl->first + 3 * cta + 2);
+    i = a.x;
+    kv = a.y;
+    at = join64(a.z, a.w);
+    nx = join64(b.x, b.y);
+    t.b = raw.x; t.tok0 = raw.y; t.ntok = raw.z; t.lim0 = raw.w;
   }
   __device__ __forceinline__ void init_whole(const RowPlan* pl, int tiles_, int cta, int ctas, int units_, int key_tile_,
                                              int causal_) {

@@ -575,15 +575,19 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       // its tokens see are zeroed where they are not finite. A token that does see such a row gets
       // its NaN through the score, whose MMA has read the tile before it is patched.
       // This warp also walks the plan and hands the unit parts out, two ahead of the one it is at.
+      const int4 h1 = __ldg(reinterpret_cast<const int4*>(p.plan.hdr) + 1);
       const int tiles = __ldg(p.plan.hdr);
       UnitWalk walk;
-      const Stretch st = stretch_of(__ldg(p.plan.start + tiles), blockIdx.x, gridDim.x);
+      Stretch st;
+      st.quota = join64(h1.x, h1.y);
+      st.lo = min((long long)blockIdx.x * st.quota, join64(h1.z, h1.w));
+      st.hi = min(st.lo + st.quota, join64(h1.z, h1.w));
       // Per-head form, many units: whole ones in turn, so that the CTAs work on a few heads of one
       // sequence at a time, whose keys and values L2 holds (with stretches each streams its own from
       // memory: 30 GB read for one 16384-token prompt of 128 heads, 11.1 ms)
       const bool whole_units = SPLIT && tiles * p.nsub >= 8 * (int)gridDim.x;
       if (whole_units) walk.init_whole(&p.plan, tiles, blockIdx.x, gridDim.x, p.nsub, KT, p.causal);
-      else walk.init(&p.plan, tiles, st, p.nsub * Sh::HALVES, KT, p.causal);
+      else walk.init(&p.plan, tiles, st, blockIdx.x, p.nsub * Sh::HALVES, KT, p.causal);
       uint32_t given = 0;
       bool more = true;
       auto give = [&]() {
@@ -909,19 +913,27 @@ __global__ void __launch_bounds__(256) mlra_rows_merge_kernel(const MergeParams 
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    for (int x = c0; x <= c1; ++x) {
-      const size_t at = (size_t)(2 * x + (x == c0 ? 1 : 0)) * p.rows + r;
-      const float lv = __ldg(p.part_lse + at);
-      float v[8];
+    for (int x0 = c0; x0 <= c1; x0 += 4) {
+      // four parts' loads under way
+      float lv[4], v[4][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = e < per ? __ldg(p.part_o + at * p.dv + e * 32 + lane) : 0.f;
-      if (lv == -INFINITY) continue;
-      const float mn = fmaxf(mx, lv);
-      const float a = fast_exp2(mx - mn), w = fast_exp2(lv - mn);
-      sum = sum * a + w;
+      for (int g = 0; g < 4; ++g) {
+        const int x = x0 + g;
+        const size_t at = (size_t)(2 * x + (x == c0 ? 1 : 0)) * p.rows + r;
+        lv[g] = x <= c1 ? __ldg(p.part_lse + at) : -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + w * v[e];
-      mx = mn;
+        for (int e = 0; e < 8; ++e) v[g][e] = x <= c1 && e < per ? __ldg(p.part_o + at * p.dv + e * 32 + lane) : 0.f;
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (lv[g] == -INFINITY) continue;
+        const float mn = fmaxf(mx, lv[g]);
+        const float a = fast_exp2(mx - mn), w = fast_exp2(lv[g] - mn);
+        sum = sum * a + w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + w * v[g][e];
+        mx = mn;
+      }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int head = (sub / p.chunks) * p.heads_block + (sub % p.chunks) * p.heads_tile + hr;
@@ -971,7 +983,7 @@ struct UpShape {
 struct UpParams {
   const int* used;       // tokens in use (rows past them are left as they were)
   void* out;             // [tokens][heads][DH]
-  int out_f32, heads;
+  int out_f32, heads, total;  // total: tokens of the call
   float out_scale;
   int* status;
   unsigned long long wait_limit_ns;
@@ -1022,6 +1034,22 @@ __global__ void __launch_bounds__(Sh::THREADS)
     *drain_err = 0;
     fence_mbar_init();
   }
+  const int seq_tiles = EXPAND ? (p.pt_stride + 1) / 2 : 1;  // token tiles of a sequence's table row
+  const int tiles = EXPAND ? p.batch * seq_tiles : (p.total + 127) / 128;
+  const long long items = (long long)tiles * p.heads * (EXPAND ? 2 : 1);
+  const long long per = (items + gridDim.x - 1) / gridDim.x;
+  const long long lo = min(per * blockIdx.x, items), hi = min(lo + per, items);
+  auto load_weight = [&](int h) {
+    const uint64_t keep = l2_policy_evict_last();
+    mbar_arrive_expect_tx(wfull, Sh::W_BYTES);
+    for (int a = 0; a < Sh::NATOM; ++a)
+      for (int j = 0; j < Sh::SUMK; ++j)
+        for (int r = 0; r < Sh::DBB; r += Sh::WBOX)
+          tma_load_2d(wbuf + a * Sh::ATOM + (j * Sh::DBB + r) * Sh::WROWB, EXPAND && (h & 1) ? &map_w2 : &map_w, wfull,
+                      a * Sh::AW, (EXPAND ? h / 2 : j * p.heads + h) * Sh::DBB + r, keep);
+  };
+  // the first head's weight does not depend on the kernel before
+  if (!EXPAND && threadIdx.x == 0 && lo < hi) load_weight((int)(lo / tiles));
   grid_dependency_wait();
   if (warp == 1) {
     tmem_alloc(tmem_slot, Sh::TMEM_COLS);
@@ -1035,22 +1063,22 @@ __global__ void __launch_bounds__(Sh::THREADS)
 
   if (EXPAND && blockIdx.x == 0 && threadIdx.x == 0) clear_status_and_tags(p.status, p.tags);
   const int used = EXPAND ? 0 : __ldg(p.used);
-  const int seq_tiles = EXPAND ? (p.pt_stride + 1) / 2 : 1;  // token tiles of a sequence's table row
-  const int tiles = EXPAND ? p.batch * seq_tiles : (used + 127) / 128;
-  const long long items = (long long)tiles * p.heads * (EXPAND ? 2 : 1);
   auto length = [&](int b) { return min(max(__ldg(p.lens + b), 0), p.pt_stride * kPage); };
   // EXPAND: whether the tile lies past its sequence's end
   auto skip = [&](int tile) {
     return EXPAND && (tile % seq_tiles) * 128 >= length(tile / seq_tiles);
   };
-  const long long per = (items + gridDim.x - 1) / gridDim.x;
-  const long long lo = min(per * blockIdx.x, items), hi = min(lo + per, items);
 
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_first(), keep = l2_policy_evict_last();
       uint32_t c = 0, wc = 0, issued = 0, parity = 0;
       int w_parity = -1, head = -1;
+      if (!EXPAND && lo < hi) {
+        head = (int)(lo / tiles);
+        w_parity = 0;
+        wc = 1;
+      }
       bool ok = true;
       for (long long it = lo; it < hi && ok; ++it) {
         const int h = (int)(it / tiles), tile = (int)(it % tiles), tok = tile * 128;
@@ -1071,13 +1099,8 @@ __global__ void __launch_bounds__(Sh::THREADS)
           head = h;
           ok = mbar_wait(wfree, (wc & 1) ^ 1, abort_flag, p.wait_limit_ns);
           if (!ok) break;
-          mbar_arrive_expect_tx(wfull, Sh::W_BYTES);
+          load_weight(h);
           w_parity = wc & 1;
-          for (int a = 0; a < Sh::NATOM; ++a)
-            for (int j = 0; j < Sh::SUMK; ++j)
-              for (int r = 0; r < Sh::DBB; r += Sh::WBOX)
-                tma_load_2d(wbuf + a * Sh::ATOM + (j * Sh::DBB + r) * Sh::WROWB, EXPAND && (h & 1) ? &map_w2 : &map_w,
-                            wfull, a * Sh::AW, (EXPAND ? h / 2 : j * p.heads + h) * Sh::DBB + r, keep);
           ++wc;
         }
         for (int kc = 0; kc < NKC && ok; ++kc, ++c) {

@@ -128,16 +128,17 @@ struct RowsWorkspace {
 // Plan and partial slots of the row attention over `tokens` query tokens of `seqs` sequences;
 // `heads`: heads a row tile stacks.
 template <class Sh>
-RowsWorkspace carve_rows(const mlra_ctx* h, Carver& c, size_t tokens, size_t seqs, int heads, bool tok_tile) {
+RowsWorkspace carve_rows(const mlra_ctx* h, Carver& c, size_t tokens, size_t seqs, int heads, bool per_token) {
   const size_t tile = (size_t)Sh::NQ * (128 / heads);
   const size_t tiles = tokens / tile + seqs;
   RowsWorkspace w;
-  w.plan.hdr = c.take<int>(4);
+  w.plan.hdr = c.take<int>(8);
+  w.plan.first = c.take<int4>((size_t)3 * h->num_sms);
   w.plan.start = c.take<long long>(tiles + 1);
   w.plan.tile = c.take<TokenTile>(tiles);
   w.plan.base = c.take<int>(seqs + 1);
   w.plan.cut = c.take<int4>((size_t)2 * h->num_sms);
-  w.plan.tok_tile = tok_tile ? c.take<int>(tokens) : nullptr;
+  w.plan.tok = per_token ? c.take<int4>(tokens) : nullptr;
   w.part_lse = c.take<float>((size_t)2 * h->num_sms * Sh::ROWS);
   w.part_o = c.take<float>((size_t)2 * h->num_sms * Sh::ROWS * Sh::DV);
   return w;
@@ -270,6 +271,7 @@ cudaError_t launch_plan(const mlra_ctx* h, const RowsCall& c, int* status, cudaS
   p.total_q = c.tokens;
   p.cap_len = c.pt_stride * kPage;
   p.causal = c.causal;
+  p.ctas = h->num_sms;
   p.plan = c.rp.plan;
   p.status = status;
   p.tile_tokens = Sh::NQ * (128 / (Sh::SPLIT ? 1 : heads_tile_of(h)));
@@ -545,6 +547,7 @@ int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t*
     up.out = out;
     up.out_f32 = out_dtype == MLRA_F32;
     up.heads = h->cfg.h;
+    up.total = total_q;
     up.out_scale = h->summed ? h->alpha : 1.f;
     up.status = w.status;
     up.wait_limit_ns = kWaitLimitNs;
