@@ -317,6 +317,13 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
   };
   // row tiles a unit part uses
   auto rows_of = [&](const UnitPart& x) { return NQ == 2 && x.t.ntok > p.tok_tile ? 2 : 1; };
+  // key tiles of the part that row tile q sees any of: the first row tile's tokens may all lie before
+  // the part's last key tiles, which are then formed for the second one alone
+  auto tiles_of_row = [&](const UnitPart& x, int q) {
+    const int last = min(x.t.ntok, (q + 1) * p.tok_tile) - 1;
+    const int lim = max(p.causal ? x.t.lim0 + last : x.t.lim0, 0);
+    return max(min(x.end, (lim + KT - 1) / KT) - x.begin, 0);
+  };
   UnitPart u;
   // (the register split sits in the two branches, so that each is compiled for its own share)
   if (warp >= 4 * NQ) {
@@ -468,12 +475,19 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       int last = -1;            // two row tiles: whose scores the buffer holds
       bool ok = true;
       while (ok && take(u)) {
-        const int n = u.end - u.begin, nrow = rows_of(u);
+        const int n = u.end - u.begin, nrow = rows_of(u), n0 = tiles_of_row(u, 0);
+        if (n0 == 0) {
+          // a part whose first row tile sees none of it: its query is given back unread
+          ok = wait(&qfull[0], qc[0] & 1);
+          ++qc[0];
+          if (one) umma_commit(&qempty[0]);
+        }
         for (int i = 0; i < n && ok; ++i, ++kt) {
           ok = wait(&kfull[kt % CST], (kt / CST) & 1);
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             if (q >= nrow || !ok) break;
+            if (NQ == 2 && q == 0 && i >= n0) continue;
             if (i == 0) {
               ok = wait(&qfull[q], qc[q] & 1);
               ++qc[q];
@@ -505,7 +519,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
                   umma_ss(d, a0 + ((Sh::NC * Sh::QC_REG + r * Sh::QR_REG + ks * 32) >> 4), r_hi,
                           b1 + ((r * Sh::KR_REG + ks * 32) >> 4), r_hi, idesc_qk, 1u);
               umma_commit(&sfull[NQ == 1 ? kt & 1 : q]);
-              if (i == n - 1) umma_commit(&qempty[q]);
+              if (i == (q == 0 ? n0 : n) - 1) umma_commit(&qempty[q]);
               if (q == nrow - 1) {
                 umma_commit(SPLIT ? &cempty[kt % CST] : &rempty[kt % RST]);
                 // a tile that reaches past what the part's first token sees is patched (see the patch
@@ -531,16 +545,18 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       for (int q = 0; q < NQ; ++q) pc[q] = oc[q] = 0;
       bool ok = true;
       while (ok && take(u)) {
-        const int n = u.end - u.begin, nrow = rows_of(u);
+        const int n = u.end - u.begin, nrow = rows_of(u), n0 = tiles_of_row(u, 0);
         const uint32_t half = (u.sub % Sh::HALVES) * ((DV / Sh::CW) * (Sh::KC_REG >> 4));
         for (int i = 0; i < n && ok; ++i, ++kt) {
           if constexpr (SPLIT) ok = wait(&vfull[kt % PST], (kt / PST) & 1);
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             if (q >= nrow || !ok) break;
+            if (NQ == 2 && q == 0 && i >= n0) continue;
             ok = wait(&pfull[q], pc[q] & 1);
             ++pc[q];
-            if (!SPLIT && q == 0 && (u.begin + i + 1) * KT > u.t.lim0) {
+            // (the tile's first reader waits for its patch)
+            if (!SPLIT && q == (NQ == 2 && i >= n0 ? 1 : 0) && (u.begin + i + 1) * KT > u.t.lim0) {
               ok = ok && wait(&patched[kt % PST], (fixes >> (kt % PST)) & 1);
               fixes ^= 1u << (kt % PST);
             }
@@ -592,6 +608,14 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       bool more = true;
       auto give = [&]() {
         const UnitPart g = whole_units ? walk.next_whole() : walk.next();
+        const int e = given % Sh::PARTS;
+        if (!wait(&pread[e], ((given / Sh::PARTS) & 1) ^ 1)) return false;
+        if (lane == 0) {
+          parts[3 * e] = make_int4(g.t.b, g.t.tok0, g.t.ntok, g.t.lim0);
+          parts[3 * e + 1] = make_int4(g.sub, g.kv, g.begin, g.end);
+          parts[3 * e + 2].x = g.valid;
+          mbar_arrive(&pready[e]);
+        }
         if (given == 0 && lane == 0) {
           // for the merge: the unit that this stretch goes on with, and the CTAs that share it
           int c0 = -1, c1 = -1;
@@ -602,14 +626,6 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
           }
           p.plan.cut[2 * blockIdx.x] = make_int4(c0, c1, g.sub, 0);
           p.plan.cut[2 * blockIdx.x + 1] = make_int4(g.t.tok0, g.t.ntok, 0, 0);
-        }
-        const int e = given % Sh::PARTS;
-        if (!wait(&pread[e], ((given / Sh::PARTS) & 1) ^ 1)) return false;
-        if (lane == 0) {
-          parts[3 * e] = make_int4(g.t.b, g.t.tok0, g.t.ntok, g.t.lim0);
-          parts[3 * e + 1] = make_int4(g.sub, g.kv, g.begin, g.end);
-          parts[3 * e + 2].x = g.valid;
-          mbar_arrive(&pready[e]);
         }
         __syncwarp();
         ++given;
@@ -695,8 +711,8 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
     bool ok = true;
     const float sc_mul = p.s_scale, slack = 8.f / sc_mul;
     while (ok && take(u)) {
-      const int n = u.end - u.begin;
       if (q >= rows_of(u)) continue;
+      const int n = tiles_of_row(u, q);
       const int lim = p.causal ? u.t.lim0 + tok : u.t.lim0;  // keys this row sees
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i, ++sc) {
@@ -714,10 +730,10 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         const int k0 = (u.begin + i) * KT;
         if (k0 + KT > u.t.lim0) {
           // 16 keys at a time: those every row of the warp sees are left alone
-          const int seen = lim - k0;
+          const int seen = lim - k0, all = __reduce_min_sync(0xffffffffu, seen);
 #pragma unroll
           for (int c0 = 0; c0 < KT; c0 += 16) {
-            if (__all_sync(0xffffffffu, seen >= c0 + 16)) continue;
+            if (all >= c0 + 16) continue;
 #pragma unroll
             for (int c = c0; c < c0 + 16; ++c) s[c] = c < seen ? s[c] : -INFINITY;
           }
@@ -781,7 +797,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         if (lane == 0) mbar_arrive(&pfull[q]);
       }
       if (!ok) break;
-      ok = wait(&pvdone[q], (sc - 1) & 1);
+      if (n > 0) ok = wait(&pvdone[q], (sc - 1) & 1);
       if (!ok) break;
       tc_fence_after();
       // ---- results of this part ----
@@ -806,8 +822,9 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         float o[32];
         tmem_load_row<32>(o_addr + c, o);
         tmem_ld_wait();
+        // (a row tile without a key tile in this part has no O)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= inv;
+        for (int e = 0; e < 32; ++e) o[e] = n > 0 ? o[e] * inv : 0.f;
         if (whole && p.o_bf16 != nullptr) {
           uint4 v4[4];
 #pragma unroll
@@ -843,7 +860,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ofree[q]);
+      if (n > 0 && lane == 0) mbar_arrive(&ofree[q]);
     }
   }
   tc_fence_before();

@@ -38,6 +38,10 @@ cudaError_t prep_head() {
   return e == cudaSuccess ? prep_kernel(mlra_rows_kernel<RowsHead>, RowsHead::SMEM) : e;
 }
 cudaError_t prep_rows(Variant v) {
+  cudaError_t e0 = prep_kernel(mlra_rows_plan_kernel, 0);
+  if (e0 == cudaSuccess) e0 = prep_kernel(mlra_rows_merge_kernel, 0);
+  if (e0 == cudaSuccess) e0 = prep_kernel(mlra_widen_pages_kernel, 0);
+  if (e0 != cudaSuccess) return e0;
   cudaError_t e = with_rows(v, [](auto sh) {
     using Sh = decltype(sh);
     return prep_kernel(mlra_rows_kernel<Sh>, Sh::SMEM);
