@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
 #pragma unroll
       for (int q = 0; q < NQ; ++q) qc[q] = 0;
       // the part's queries (behind its first key tile, whose place is free earlier); one lane
-      auto load_queries = [&](int sub, int nrow) {
-        const int rows = p.heads_tile * p.tok_tile;
+      auto load_queries = [&](const UnitPart& x) {
+        const int rows = p.heads_tile * p.tok_tile, sub = x.sub / Sh::HALVES, nrow = rows_of(x);
         for (int q = 0; q < nrow; ++q) {
           if (!mbar_wait(&qempty[q], (qc[q] & 1) ^ 1, abort_flag, p.wait_limit_ns)) return false;
           mbar_arrive_expect_tx(&qfull[q], rows * (Sh::DB + Sh::DR) * 2);
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
           q_parity = (q_parity & ~(1u << q)) | ((qc[q] & 1) << q);
           ++qc[q];
           uint8_t* dst = qbuf + q * Sh::Q_BYTES;
-          const int tok = u.t.tok0 + q * p.tok_tile;
+          const int tok = x.t.tok0 + q * p.tok_tile;
           for (int r = 0; r < Sh::NC; ++r)
             tma_load_4d(dst + r * Sh::QC_REG, &map_qc, &qfull[q], r * Sh::CW, 0, sub, tok, pol);
           for (int r = 0; r < Sh::NR; ++r)
@@ -361,42 +361,50 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         par = (par & ~(1u << s)) | (ph << s);
       };
       bool ok = true;
-      while (ok && take(u)) {
-        const int sub = u.sub / Sh::HALVES;
-        const int nrow = rows_of(u);
-        if constexpr (SPLIT) {
-          // keys a tile ahead of values, whose place comes free later
-          const int r0 = u.t.b * p.seq_rows, y0 = sub * p.kv_rows + r0;
-          if (lane == 0) {
-            auto load_keys = [&](int t, uint32_t n) {
-              const int s = n % CST;
-              const uint32_t ph = (n / CST) & 1;
-              if (!mbar_wait(&cempty[s], ph ^ 1, abort_flag, p.wait_limit_ns)) return false;
-              mbar_arrive_expect_tx(&kfull[s], Sh::C_BYTES + Sh::R_BYTES);
-              note(issued, parity, s, ph);
-              for (int r = 0; r < Sh::NC; ++r)
-                tma_load_2d(cring + s * Sh::C_BYTES + r * Sh::KC_REG, &map_c, &kfull[s], r * Sh::CW, y0 + t * KT, pol);
-              for (int r = 0; r < Sh::NR; ++r)
-                tma_load_2d(rring + s * Sh::R_BYTES + r * Sh::KR_REG, &map_r, &kfull[s], r * Sh::RW, r0 + t * KT, pol);
-              return true;
-            };
-            ok = load_keys(u.begin, kt) && load_queries(sub, nrow);
-            for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
-              if (t + 1 < u.end) ok = load_keys(t + 1, kt + 1);
+      if constexpr (SPLIT) {
+        // Keys go a tile ahead of values, whose place comes free later, and a part's first keys and its
+        // queries ahead of the last values of the part before.
+        auto load_keys = [&](const UnitPart& x, int t, uint32_t n) {
+          const int s = n % CST, r0 = x.t.b * p.seq_rows + t * KT, y = x.sub * p.kv_rows + r0;
+          const uint32_t ph = (n / CST) & 1;
+          if (!mbar_wait(&cempty[s], ph ^ 1, abort_flag, p.wait_limit_ns)) return false;
+          mbar_arrive_expect_tx(&kfull[s], Sh::C_BYTES + Sh::R_BYTES);
+          note(issued, parity, s, ph);
+          for (int r = 0; r < Sh::NC; ++r)
+            tma_load_2d(cring + s * Sh::C_BYTES + r * Sh::KC_REG, &map_c, &kfull[s], r * Sh::CW, y, pol);
+          for (int r = 0; r < Sh::NR; ++r)
+            tma_load_2d(rring + s * Sh::R_BYTES + r * Sh::KR_REG, &map_r, &kfull[s], r * Sh::RW, r0, pol);
+          return true;
+        };
+        UnitPart v;
+        bool more = take(u);
+        if (more && lane == 0) ok = load_keys(u, u.begin, 0) && load_queries(u);
+        while (more && __shfl_sync(0xffffffffu, ok, 0)) {
+          bool next = false;
+          for (int t = u.begin; t < u.end; ++t, ++kt) {
+            const bool last = t + 1 == u.end;
+            if (last) next = take(v);
+            if (lane == 0 && ok) {
+              if (!last) ok = load_keys(u, t + 1, kt + 1);
+              else if (next) ok = load_keys(v, v.begin, kt + 1) && load_queries(v);
               const int s = kt % PST;
               const uint32_t ph = (kt / PST) & 1;
               ok = ok && mbar_wait(&vempty[s], ph ^ 1, abort_flag, p.wait_limit_ns);
-              if (!ok) break;
-              mbar_arrive_expect_tx(&vfull[s], Sh::V_BYTES);
-              note(v_issued, v_parity, s, ph);
-              for (int r = 0; r < DV / Sh::CW; ++r)
-                tma_load_2d(vring + s * Sh::V_BYTES + r * Sh::KC_REG, &map_c, &vfull[s], Sh::DB + r * Sh::CW,
-                            y0 + t * KT, pol);
+              if (ok) {
+                mbar_arrive_expect_tx(&vfull[s], Sh::V_BYTES);
+                note(v_issued, v_parity, s, ph);
+                for (int r = 0; r < DV / Sh::CW; ++r)
+                  tma_load_2d(vring + s * Sh::V_BYTES + r * Sh::KC_REG, &map_c, &vfull[s], Sh::DB + r * Sh::CW,
+                              u.sub * p.kv_rows + u.t.b * p.seq_rows + t * KT, pol);
+              }
             }
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          continue;
+          u = v;
+          more = next;
         }
+      }
+      while (!SPLIT && ok && take(u)) {
+        const int sub = u.sub / Sh::HALVES;
         const int blk = sub / p.chunks;
         const int pages = (tile_limit(u.t, p.causal) + kPage - 1) / kPage;
         const size_t row = (size_t)u.t.b * p.pt_stride;
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
                               p.d_c + r * Sh::RW, y, pol);
               }
             }
-            if (t == u.begin) ok = ok && load_queries(sub, nrow);
+            if (t == u.begin) ok = ok && load_queries(u);
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
         }
