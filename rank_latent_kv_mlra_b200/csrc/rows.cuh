@@ -979,6 +979,8 @@ __global__ void __launch_bounds__(256) mlra_rows_merge_kernel(const MergeParams 
 // K = SUMK * d_b (summed blocks: the blocks' latents and weights stacked along K); A tiles of 64
 // columns come through a ring, two accumulators alternate. Bound by memory: it reads o~ and writes
 // out once, 512 bytes for 2 * 128 * 128 FLOPs.
+constexpr float kMaxBf16 = 3.3895314e38f;  // the largest bf16 value
+
 template <int DBB_, int DH_, int SUMK_>
 struct UpShape {
   static constexpr int DBB = DBB_, DH = DH_, SUMK = SUMK_, K = DBB * SUMK;
@@ -993,7 +995,9 @@ struct UpShape {
   static constexpr int OFF_RING = W_BYTES;
   static constexpr int OFF_BAR = OFF_RING + STAGES * A_REG;
   static constexpr int SMEM = OFF_BAR + (2 * STAGES + 2 + 4 + 1) * 8 + 64 + 1024;
-  static constexpr int THREADS = 192;
+  // loads, MMAs, and two groups of four warps that each take half of the result's columns (with one
+  // group the expansion of 24,800 tokens took 533 us, bound by its latency)
+  static constexpr int THREADS = 320;
   static_assert(W_BYTES % 1024 == 0 && A_REG % 1024 == 0 && SMEM <= 227 * 1024, "layout");
 };
 
@@ -1002,8 +1006,8 @@ struct UpShape {
 // the table row's pages, rounded up to whole 128-token tiles, all of which are written); a weight is
 // then one of a head's two. Reads the rows once a weight (from L2 after the first), writes 512 bytes
 // a token and head. The blocks also copy the RoPE columns to rows of their own.
-// Values are stored finite, infinities as the largest bf16 value and NaN as 0: a masked key's P = 0
-// then adds nothing. A token that does see a cached row with NaN or infinities gets NaN through the
+// Values are stored finite, infinities and NaN as the largest bf16 values: a masked key's P = 0 then
+// adds nothing. A token that does see a cached row with NaN or infinities gets NaN through the
 // row's keys, which keep them.
 struct UpParams {
   const int* used;       // tokens in use (rows past them are left as they were)
@@ -1052,7 +1056,7 @@ __global__ void __launch_bounds__(Sh::THREADS)
     mbar_init(wfree, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&dfull[i], 1);
-      mbar_init(&dfree[i], 4);
+      mbar_init(&dfree[i], 8);
     }
     mbar_init(drained, 1);
     *abort_flag = 0;
@@ -1199,13 +1203,13 @@ __global__ void __launch_bounds__(Sh::THREADS)
     uint32_t n = 0;
     if constexpr (EXPAND) {
       // RoPE columns of the pages, 16 bytes a thread
-      const int cpr = p.d_r / 8, tid = threadIdx.x - 64;
+      const int cpr = p.d_r / 8, tid = threadIdx.x - 64;  // 256 threads
       for (int pg = blockIdx.x; pg < p.batch * p.pt_stride; pg += gridDim.x) {
         const int b = pg / p.pt_stride;
         if ((pg - b * p.pt_stride) * kPage >= length(b)) continue;
         int id = __ldg(p.page_table + pg);
         if (id < 0 || id >= p.num_pages) id = 0;  // (reported by the loads)
-        for (int i = tid; i < kPage * cpr; i += 128) {
+        for (int i = tid; i < kPage * cpr; i += Sh::THREADS - 64) {
           const int r = i / cpr, x = (i % cpr) * 8;
           const size_t at = (size_t)b * p.seq_rows + (pg - b * p.pt_stride) * kPage + r;
           *reinterpret_cast<uint4*>(p.kr + at * p.d_r + x) = __ldg(
@@ -1218,8 +1222,11 @@ __global__ void __launch_bounds__(Sh::THREADS)
       if (skip(tile)) continue;
       if (!__all_sync(0xffffffffu, mbar_wait(&dfull[n & 1], (n >> 1) & 1, abort_flag, p.wait_limit_ns))) break;
       tc_fence_after();
+      const int c0 = ((warp - 2) >> 2) * (DH / 2 < 32 ? 32 : DH / 2);
 #pragma unroll
-      for (int c = 0; c < DH; c += 32) {
+      for (int ci = 0; ci < (DH / 2 < 32 ? 32 : DH / 2); ci += 32) {
+        const int c = c0 + ci;
+        if (c >= DH) break;
         float v[32];
         tmem_load_row<32>(tbase + lane_base + (n & 1) * DH + c, v);
         tmem_ld_wait();
@@ -1228,16 +1235,17 @@ __global__ void __launch_bounds__(Sh::THREADS)
           for (int e = 0; e < 32; ++e) v[e] *= p.out_scale;
         }
         if constexpr (EXPAND) {
-          if (h & 1) {
-            constexpr float kMax = 3.3895314e38f;  // the largest bf16 value
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = v[e] == v[e] ? fminf(fmaxf(v[e], -kMax), kMax) : 0.f;
-          }
           uint4 v4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             v4[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
                                pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+          if (h & 1) {  // max and min pass a NaN over
+            const __nv_bfloat162 top = __floats2bfloat162_rn(kMaxBf16, kMaxBf16), low = __hneg2(top);
+            __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(v4);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) h2[e] = __hmin2(__hmax2(h2[e], low), top);
+          }
           exchange4(v4, lane);
           const int b = tile / seq_tiles, t0 = (tile % seq_tiles) * 128 + (row & ~3);
           __nv_bfloat16* dst = p.kv + ((size_t)(h / 2) * p.kv_rows + (size_t)b * p.seq_rows + t0) * (2 * DH) +
