@@ -160,6 +160,42 @@ def test_full_pool_and_many_rows():
     assert both.fork([1] * 200, list(range(0, 600, 3))) == 0
 
 
+def test_large_pool_without_its_contents():
+    """300,000 pages (37 stretches of the bitmap), counts and tables only."""
+    P, R, S = 300000, 200, 1500
+    both = Both(TINY, 1, 1, 1)
+    refs = torch.zeros(P, dtype=torch.int32, device="cuda")
+    table = torch.full((R, S), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(R, dtype=torch.int32, device="cuda")
+    model = PagesModel(refs.cpu().numpy(), table.cpu().numpy(), lens.cpu().numpy())
+    rng = random.Random(7)
+    for step in range(6):
+        ids = rng.sample(range(R), 120)
+        new = [rng.randint(int(model.lens[i]), S * 64) for i in ids]
+        ws = M.mlra_reserve_pages(both.handle, refs, table, lens, i32(ids), i32(new))
+        assert M.mlra_get_status(ws) == model.reserve(ids, new)
+        gone = rng.sample(range(R), 60)
+        ws = M.mlra_free_pages(both.handle, refs, table, lens, i32(gone))
+        assert M.mlra_get_status(ws) == model.free(gone)
+        assert np.array_equal(refs.cpu().numpy(), model.refs) and np.array_equal(table.cpu().numpy(), model.table)
+        assert np.array_equal(lens.cpu().numpy(), model.lens)
+
+
+def test_refused_arguments():
+    both = Both(TINY, 40, 6, 8, seed=8)
+    with pytest.raises(ValueError, match="one length"):
+        M.mlra_reserve_pages(both.handle, *both.state, i32([1, 2]), i32([5]))
+    with pytest.raises(M.MlraError, match="INVALID_ARG"):   # more requests than rows
+        M.mlra_free_pages(both.handle, *both.state, i32([0] * 7))
+    with pytest.raises(ValueError, match="pool must be"):
+        M.mlra_compact_pages(both.handle, both.pool[:39], *both.state)
+    with pytest.raises(TypeError, match="refs"):
+        M.mlra_free_pages(both.handle, both.refs.long(), both.table, both.lens, i32([0]))
+    ws = torch.empty(M.mlra_pages_workspace_size(both.handle, 40, 6) - 256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(M.MlraError, match="WORKSPACE"):
+        M.mlra_free_pages(both.handle, *both.state, i32([0]), workspace=ws)
+
+
 def test_bad_table_entries_are_passed_over():
     both = Both(TINY, 40, 6, 8, seed=5)
     both.reserve([0, 1], [200, 200])

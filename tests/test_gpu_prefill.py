@@ -156,6 +156,13 @@ CASES = {
     "prompts_rank4": (RANK4, [700, 513, 64, 300], [0, 5, 200, 0]),
     "prompt_one_odd_page": (MLRA4, [65], [0]),
     "prompt_three_units": (MLA, [700], [0]),
+    "prompts_whole_units": (MLRA4, [1500, 0, 1, 900, 257, 0], [0, 0, 0, 60, 0, 5]),
+    # heads of a block that do not divide a row tile, and one head a block
+    "heads3": (W.scaled(MLRA4, h=12), [1, 41, 42, 43, 84, 85, 130], [0, 3, 700, 0, 64, 1, 0]),
+    "heads1": (W.scaled(MLRA4, h=4), [1, 127, 300], [65, 0, 500]),
+    "prompts_heads3": (W.scaled(MLRA4, h=12), [300, 41, 130], [0, 0, 0]),
+    "rank_heads": (W.scaled(RANK4, h=96), [5, 130], [40, 200]),   # three chunks of 32 heads
+    "mlra2_heads5": (W.scaled(MLRA2, h=10), [1, 25, 26, 130], [0, 3, 700, 0]),
 }
 FORMS = [(name, None) for name in CASES if not name.startswith("prompt")] + [
     (name, form) for name in CASES if name.startswith("prompt") for form in ("absorbed", "heads")]
@@ -170,9 +177,85 @@ def test_matches_the_definition(name, form):
         check(w, inp, *run(hdl, w, inp, dt), f"{name} {dt}")
 
 
-def test_fp32_query():
-    w, inp = make(MLRA4, [40, 3], [0, 90], seed=5, q_dtype=torch.float32)
-    check(w, inp, *run(handle(w, inp), w, inp), "fp32 query")
+@pytest.mark.parametrize("n,past", [([40, 3], [0, 90]), ([300, 129], [0, 0])], ids=["chunk", "prompts"])
+def test_fp32_query(n, past):
+    """(An fp32 query of whole prompts takes the absorbed form in a workspace sized for both.)"""
+    w, inp = make(MLRA4, n, past, seed=5, q_dtype=torch.float32)
+    hdl = handle(w, inp)
+    check(w, inp, *run(hdl, w, inp), "fp32 query")
+    size = M.mlra_prefill_workspace_size(hdl, sum(n), len(n), inp["page_table"].shape[1])
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    check(w, inp, *run(hdl, w, inp, workspace=ws), "fp32 query, own workspace")
+    with pytest.raises(M.MlraError, match="WORKSPACE"):
+        run(hdl, w, inp, workspace=ws[:size - 256])
+
+
+def test_e4m3_cache_with_two_scales():
+    """Different latent and RoPE scales, neither a power of two (outputs and lse of the same bytes)."""
+    w, inp = make(E4M3, [70, 33], [0, 200], seed=15)
+    lat, rope = 0.03, 0.05
+    hdl = M.mlra_create(w.h, w.d_h, w.d_c, w.d_r, w.k, inp["w_uk"], inp["w_uv"], cache_fp8=True, latent_scale=lat,
+                        rope_scale=rope)
+    out, lse, status = run(hdl, w, inp)
+    # reference: a bf16-free cache of the values the bytes stand for
+    plain = dict(inp)
+    vals = inp["pool"].view(torch.float8_e4m3fn).double()
+    plain["pool"] = torch.cat([vals[..., :w.d_c] * lat, vals[..., w.d_c:] * rope], dim=-1)
+    check(W.scaled(w, cache="bf16"), plain, out, lse, status, "two scales")
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Calls on two streams with workspaces of their own give what each gives alone."""
+    runs = []
+    for seed, form in ((21, "heads"), (22, "absorbed")):
+        w, inp = make(MLRA4, [700, 300], [0, 0], seed=seed, form=form)
+        hdl = handle(w, inp)
+        runs.append((w, inp, hdl, run(hdl, w, inp)[0]))
+    streams = [torch.cuda.Stream() for _ in runs]
+    outs = [torch.empty_like(r[3]) for r in runs]
+    torch.cuda.synchronize()
+    words = []
+    for _ in range(5):
+        for (w, inp, hdl, _), s, out in zip(runs, streams, outs):
+            words.append(M.mlra_prefill(hdl, inp["q"], inp["cu"], inp["pool"], inp["page_table"], inp["seq_lens"], out,
+                                        stream=s))
+    torch.cuda.synchronize()
+    assert all(M.mlra_get_status(ws) == 0 for ws in words)
+    for r, out in zip(runs, outs):
+        assert torch.equal(out, r[3])
+
+
+def test_refused_arguments():
+    w, inp = make(MLRA4, [33, 90], [10, 0], seed=16)
+    hdl = handle(w, inp)
+    out = torch.empty(123, w.h, w.d_h, device="cuda")
+    args = [inp["q"], inp["cu"], inp["pool"], inp["page_table"], inp["seq_lens"], out]
+
+    def call(**kw):
+        names = ["q", "cu", "pool", "page_table", "seq_lens", "out"]
+        return M.mlra_prefill(hdl, *[kw.get(n, a) for n, a in zip(names, args)])
+
+    with pytest.raises(ValueError, match="contiguous"):
+        call(q=inp["q"].transpose(0, 1).contiguous().transpose(0, 1))
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        call(cu=inp["cu"][:2].contiguous())
+    with pytest.raises(ValueError, match="out must be"):
+        call(out=out[:100].contiguous())
+    with pytest.raises(TypeError, match="seq_lens"):
+        call(seq_lens=inp["seq_lens"].long())
+    with pytest.raises(TypeError, match="pool"):
+        call(pool=inp["pool"].float())
+    with pytest.raises(ValueError, match="one device|CUDA tensor"):
+        call(page_table=inp["page_table"].cpu())
+    shifted = torch.empty(123 * w.h * w.d_h + 1, device="cuda")[1:].view(123, w.h, w.d_h)
+    with pytest.raises(M.MlraError, match="INVALID_ARG"):  # out is not 16-byte aligned
+        call(out=shifted)
+
+
+def test_no_tokens():
+    w, inp = make(MLRA4, [0, 0], [10, 0], seed=17)
+    out, lse, status = run(handle(w, inp), w, inp)
+    assert status == 0 and out.numel() == 0
 
 
 BOTH = pytest.mark.parametrize("form", ["absorbed", "heads"])

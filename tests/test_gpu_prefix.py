@@ -108,6 +108,9 @@ CASES = {
     "mla": (MLA, [0, 3, 5], [700, 65], [0, 1, 90, 0, 5]),
     "rank4": (RANK4, [0, 3, 5], [700, 65], [0, 1, 90, 0, 5]),
     "tiny": (TINY, [0, 70, 75], [700, 65], [(i * 13) % 200 for i in range(75)]),
+    "heads3": (W.scaled(MLRA4, h=12), [0, 50, 60], [700, 65], [(i * 11) % 90 for i in range(60)]),
+    "rank_heads": (W.scaled(RANK4, h=96), [0, 3, 5], [700, 65], [0, 1, 90, 0, 5]),
+    "many_members": (MLRA4, [0, 150], [300], [i % 5 for i in range(150)]),
     "sum4": (SUM4, [0, 3, 5], [700, 65], [0, 1, 90, 0, 5]),
     "sum2": (SUM2, [0, 3, 5], [700, 65], [0, 1, 90, 0, 5]),
     "tinysum": (W.scaled(TINY, summed=True), [0, 20, 21], [300, 0], [i * 3 for i in range(21)]),
@@ -144,6 +147,31 @@ def test_large_batch_matches_decode_on_the_whole_sequences():
     torch.cuda.synchronize()
     G.assert_parity(out.cpu().numpy(), dout.double().cpu().numpy(), "prefix against whole")
     assert (lse - dlse).abs().max() < 1e-3
+
+
+def test_fp32_query_and_refusals():
+    w, inp = make(MLRA4, [0, 2, 5], [600, 200], [10, 0, 64, 100, 3], seed=8, q_dtype=torch.float32)
+    hdl = handle(w, inp)
+    check(w, inp, *run(hdl, w, inp), "fp32 query")
+    ws = torch.empty(M.mlra_decode_prefix_workspace_size(hdl, 5, 2) - 256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(M.MlraError, match="WORKSPACE"):
+        run(hdl, w, inp, workspace=ws)
+    with pytest.raises(ValueError, match="group_offsets"):
+        run(hdl, w, dict(inp, offsets=inp["offsets"][:2].contiguous()))
+    e4m3 = M.mlra_create(w.h, w.d_h, w.d_c, w.d_r, w.k, inp["w_uk"], inp["w_uv"], cache_fp8=True)
+    with pytest.raises(M.MlraError, match="UNSUPPORTED"):
+        run(e4m3, w, dict(inp, pool=torch.zeros(inp["pool"].shape, dtype=torch.uint8, device="cuda")))
+
+
+def test_a_bad_row_of_one_sequence_stays_with_it():
+    """NaN in one sequence's own row, and slots behind a prefix's end that hold NaN (as they do in
+    every workload here), leave the others' results as they were."""
+    w, inp = make(MLRA4, [0, 4], [130], [10, 20, 30, 0], seed=9)
+    hdl = handle(w, inp)
+    clean = run(hdl, w, inp)[0]
+    inp["pool"][int(inp["suf_table"][1, 0]), 5] = float("nan")
+    out = run(hdl, w, inp)[0]
+    assert torch.equal(out[[0, 2, 3]], clean[[0, 2, 3]]) and out[1].isnan().all()
 
 
 def test_more_than_256_sequences():
