@@ -981,7 +981,7 @@ __global__ void __launch_bounds__(256) mlra_rows_merge_kernel(const MergeParams 
 // out once, 512 bytes for 2 * 128 * 128 FLOPs.
 constexpr float kMaxBf16 = 3.3895314e38f;  // the largest bf16 value
 
-template <int DBB_, int DH_, int SUMK_>
+template <int DBB_, int DH_, int SUMK_, int STAGES_ = 4, bool STAGED_ = false>
 struct UpShape {
   static constexpr int DBB = DBB_, DH = DH_, SUMK = SUMK_, K = DBB * SUMK;
   static constexpr int CW = DBB < 64 ? DBB : 64, ROWB = CW * 2, NKC = K / CW;
@@ -989,11 +989,14 @@ struct UpShape {
   static constexpr int ATOM = K * WROWB;
   static constexpr int W_BYTES = NATOM * ATOM;
   static constexpr int A_REG = 128 * ROWB;
-  static constexpr int STAGES = 4;
+  static constexpr int STAGES = STAGES_;
+  static constexpr bool STAGED = STAGED_;  // results leave through shared memory (TMA stores)
+  static constexpr int OUT_BYTES = STAGED ? 2 * 128 * 128 : 0;  // two halves of 64 columns
   static constexpr int WBOX = DBB < 256 ? DBB : 256;  // rows of the weight map's box
   static constexpr int TMEM_COLS = 2 * DH < 32 ? 32 : 2 * DH;
   static constexpr int OFF_RING = W_BYTES;
-  static constexpr int OFF_BAR = OFF_RING + STAGES * A_REG;
+  static constexpr int OFF_OUT = OFF_RING + STAGES * A_REG;
+  static constexpr int OFF_BAR = OFF_OUT + OUT_BYTES;
   static constexpr int SMEM = OFF_BAR + (2 * STAGES + 2 + 4 + 1) * 8 + 64 + 1024;
   // loads, MMAs, and two groups of four warps that each take half of the result's columns (with one
   // group the expansion of 24,800 tokens took 533 us, bound by its latency)
@@ -1005,7 +1008,9 @@ struct UpShape {
 // and values c_j W^UV_h of every cached token, [head][row][K | V], row = b * seq_rows + token (seq_rows:
 // the table row's pages, rounded up to whole 128-token tiles, all of which are written); a weight is
 // then one of a head's two. Reads the rows once a weight (from L2 after the first), writes 512 bytes
-// a token and head. The blocks also copy the RoPE columns to rows of their own.
+// a token and head: TMA stores of staged tiles, because 64-byte pieces from registers cost more in
+// lane exchanges than the product (24,800 tokens of 128 heads: 535 us). The blocks also copy the RoPE
+// columns to rows of their own.
 // Values are stored finite, infinities and NaN as the largest bf16 values: a masked key's P = 0 then
 // adds nothing. A token that does see a cached row with NaN or infinities gets NaN through the
 // row's keys, which keep them.
@@ -1022,14 +1027,15 @@ struct UpParams {
   const int* page_table;
   int pt_stride, batch, num_pages, heads_block, seq_rows, kv_rows, width, d_c, d_r;
   const __nv_bfloat16* pool;
-  __nv_bfloat16* kv;     // [heads][kv_rows][2 * DH]
   __nv_bfloat16* kr;     // [kv_rows][d_r]
 };
 
 template <class Sh, bool EXPAND = false>
 __global__ void __launch_bounds__(Sh::THREADS)
     mlra_rows_up_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_w2,
-                        const __grid_constant__ CUtensorMap map_o, const UpParams p) {
+                        const __grid_constant__ CUtensorMap map_o, const __grid_constant__ CUtensorMap map_kv,
+                        const UpParams p) {
+  static_assert(EXPAND == Sh::STAGED && (!EXPAND || Sh::DH == 128), "the expansion's results are staged");
   constexpr int DH = Sh::DH, STAGES = Sh::STAGES, NKC = Sh::NKC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -1065,9 +1071,17 @@ __global__ void __launch_bounds__(Sh::THREADS)
   }
   const int seq_tiles = EXPAND ? (p.pt_stride + 1) / 2 : 1;  // token tiles of a sequence's table row
   const int tiles = EXPAND ? p.batch * seq_tiles : (p.total + 127) / 128;
-  const long long items = (long long)tiles * p.heads * (EXPAND ? 2 : 1);
-  const long long per = (items + gridDim.x - 1) / gridDim.x;
-  const long long lo = min(per * blockIdx.x, items), hi = min(lo + per, items);
+  const int items = tiles * p.heads * (EXPAND ? 2 : 1);  // (the host keeps this within 32 bits)
+  const int per = (items + gridDim.x - 1) / gridDim.x;
+  const int lo = (int)min((long long)per * blockIdx.x, (long long)items), hi = min(lo + per, items);
+  // item = head * tiles + tile, followed step by step: a division an item was most of a role's time
+  const int h_lo = tiles > 0 ? lo / tiles : 0, tile_lo = lo - h_lo * tiles;
+  auto step = [&](int& h, int& tile) {
+    if (++tile == tiles) {
+      tile = 0;
+      ++h;
+    }
+  };
   auto load_weight = [&](int h) {
     const uint64_t keep = l2_policy_evict_last();
     mbar_arrive_expect_tx(wfull, Sh::W_BYTES);
@@ -1078,7 +1092,7 @@ __global__ void __launch_bounds__(Sh::THREADS)
                       a * Sh::AW, (EXPAND ? h / 2 : j * p.heads + h) * Sh::DBB + r, keep);
   };
   // the first head's weight does not depend on the kernel before
-  if (!EXPAND && threadIdx.x == 0 && lo < hi) load_weight((int)(lo / tiles));
+  if (!EXPAND && threadIdx.x == 0 && lo < hi) load_weight(h_lo);
   grid_dependency_wait();
   if (warp == 1) {
     tmem_alloc(tmem_slot, Sh::TMEM_COLS);
@@ -1104,13 +1118,14 @@ __global__ void __launch_bounds__(Sh::THREADS)
       uint32_t c = 0, wc = 0, issued = 0, parity = 0;
       int w_parity = -1, head = -1;
       if (!EXPAND && lo < hi) {
-        head = (int)(lo / tiles);
+        head = h_lo;
         w_parity = 0;
         wc = 1;
       }
       bool ok = true;
-      for (long long it = lo; it < hi && ok; ++it) {
-        const int h = (int)(it / tiles), tile = (int)(it % tiles), tok = tile * 128;
+      int h = h_lo, tile = tile_lo;
+      for (int it = lo; it < hi && ok; ++it, step(h, tile)) {
+        const int tok = tile * 128;
         if (skip(tile)) continue;
         int id0 = 0, id1 = 0;  // EXPAND: the tile's two pages (the second may not exist)
         if (EXPAND) {
@@ -1163,9 +1178,9 @@ __global__ void __launch_bounds__(Sh::THREADS)
       uint32_t c = 0, wc = 0, n = 0;
       int head = -1;
       bool ok = true;
-      for (long long it = lo; it < hi && ok; ++it) {
-        const int h = (int)(it / tiles);
-        if (skip((int)(it % tiles))) continue;
+      int h = h_lo, tile = tile_lo;
+      for (int it = lo; it < hi && ok; ++it, step(h, tile)) {
+        if (skip(tile)) continue;
         if (h != head) {
           // the last head's MMAs free its weight
           if (head >= 0) umma_commit(wfree);
@@ -1217,24 +1232,27 @@ __global__ void __launch_bounds__(Sh::THREADS)
         }
       }
     }
-    for (long long it = lo; it < hi; ++it) {
-      const int h = (int)(it / tiles), tile = (int)(it % tiles), tok = tile * 128 + row;
+    int h = h_lo, tile = tile_lo;
+    for (int it = lo; it < hi; ++it, step(h, tile)) {
+      const int tok = tile * 128 + row;
       if (skip(tile)) continue;
-      if (!__all_sync(0xffffffffu, mbar_wait(&dfull[n & 1], (n >> 1) & 1, abort_flag, p.wait_limit_ns))) break;
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(&dfull[n & 1], (n >> 1) & 1, abort_flag, p.wait_limit_ns));
+      if (!EXPAND && !ok) break;
       tc_fence_after();
-      const int c0 = ((warp - 2) >> 2) * (DH / 2 < 32 ? 32 : DH / 2);
+      if constexpr (EXPAND) {
+        // this group's 64 columns: rows of 128 bytes in the swizzled layout of the store's box, once the
+        // last store has read the place
+        const int g = (warp - 2) >> 2;
+        uint8_t* half = smem + Sh::OFF_OUT + g * (128 * 128);
+        const bool storer = ((warp - 2) & 3) == 0 && lane == 0;
+        if (storer) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+        if (named_bar_or(1 + g, 128, !ok)) break;  // (a failed wait: the group leaves together)
 #pragma unroll
-      for (int ci = 0; ci < (DH / 2 < 32 ? 32 : DH / 2); ci += 32) {
-        const int c = c0 + ci;
-        if (c >= DH) break;
-        float v[32];
-        tmem_load_row<32>(tbase + lane_base + (n & 1) * DH + c, v);
-        tmem_ld_wait();
-        if constexpr (!EXPAND) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= p.out_scale;
-        }
-        if constexpr (EXPAND) {
+        for (int ci = 0; ci < 64; ci += 32) {
+          float v[32];
+          tmem_load_row<32>(tbase + lane_base + (n & 1) * DH + 64 * g + ci, v);
+          tmem_ld_wait();
           uint4 v4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -1246,13 +1264,37 @@ __global__ void __launch_bounds__(Sh::THREADS)
 #pragma unroll
             for (int e = 0; e < 16; ++e) h2[e] = __hmin2(__hmax2(h2[e], low), top);
           }
-          exchange4(v4, lane);
-          const int b = tile / seq_tiles, t0 = (tile % seq_tiles) * 128 + (row & ~3);
-          __nv_bfloat16* dst = p.kv + ((size_t)(h / 2) * p.kv_rows + (size_t)b * p.seq_rows + t0) * (2 * DH) +
-                               (h & 1) * DH + c + (lane & 3) * 8;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) *reinterpret_cast<uint4*>(dst + (size_t)r * 2 * DH) = v4[r];
-        } else if (p.out_f32) {
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(half + swizzle(row * 128 + ci * 2 + e * 16, 128)) = v4[e];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&dfree[n & 1]);
+        fence_proxy_async_smem();
+        named_bar_sync(1 + g, 128);
+        if (storer) {
+          const int y = (h / 2) * p.kv_rows + (tile / seq_tiles) * p.seq_rows + (tile % seq_tiles) * 128;
+          asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                           reinterpret_cast<uint64_t>(&map_kv)),
+                       "r"((h & 1) * DH + 64 * g), "r"(y), "r"(smem_u32(half))
+                       : "memory");
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        ++n;
+        continue;
+      }
+      const int c0 = ((warp - 2) >> 2) * (DH / 2 < 32 ? 32 : DH / 2);
+#pragma unroll
+      for (int ci = 0; ci < (DH / 2 < 32 ? 32 : DH / 2); ci += 32) {
+        const int c = c0 + ci;
+        if (c >= DH) break;
+        float v[32];
+        tmem_load_row<32>(tbase + lane_base + (n & 1) * DH + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] *= p.out_scale;
+        if (p.out_f32) {
           // (rows behind the last sequence, tok >= used, stay as they were)
           float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((size_t)tok * p.heads + h) * DH + c);
           if (tok < used) {
@@ -1279,6 +1321,9 @@ __global__ void __launch_bounds__(Sh::THREADS)
       if (lane == 0) mbar_arrive(&dfree[n & 1]);
       ++n;
     }
+    // stores still under way read shared memory, and later kernels read what they write
+    if (EXPAND && ((warp - 2) & 3) == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();

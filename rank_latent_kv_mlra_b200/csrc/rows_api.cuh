@@ -32,9 +32,12 @@ template <int DBB, int DH, int SUMK>
 cudaError_t prep_up() {
   return prep_kernel(mlra_rows_up_kernel<UpShape<DBB, DH, SUMK>>, UpShape<DBB, DH, SUMK>::SMEM);
 }
+// At d_b = 128 two CTAs an SM with short rings
+template <int DBB>
+using ExpandShape = UpShape<DBB, 128, 1, DBB == 128 ? 2 : 4, true>;
 template <int DBB>
 cudaError_t prep_head() {
-  cudaError_t e = prep_kernel(mlra_rows_up_kernel<UpShape<DBB, 128, 1>, true>, UpShape<DBB, 128, 1>::SMEM);
+  cudaError_t e = prep_kernel(mlra_rows_up_kernel<ExpandShape<DBB>, true>, ExpandShape<DBB>::SMEM);
   return e == cudaSuccess ? prep_kernel(mlra_rows_kernel<RowsHead>, RowsHead::SMEM) : e;
 }
 cudaError_t prep_rows(Variant v) {
@@ -350,15 +353,17 @@ cudaError_t launch_merge(const mlra_ctx* h, const RowsCall& c, cudaStream_t s) {
 
 // Keys and values of every head for the per-head form.
 template <int DBB>
-cudaError_t launch_expand(const mlra_ctx* h, const UpParams& up, cudaStream_t s) {
-  using Sh = UpShape<DBB, 128, 1>;
-  CUtensorMap mc;
-  const uint64_t D = h->cfg.d_c + h->d_r;
-  if (!make_map(&mc, up.pool, (uint64_t)up.num_pages * kPage, D, D * 2, kPage, Sh::CW)) return cudaErrorInvalidValue;
+cudaError_t launch_expand(const mlra_ctx* h, const UpParams& up, const __nv_bfloat16* kv, cudaStream_t s) {
+  using Sh = ExpandShape<DBB>;
+  CUtensorMap mc, mkv;
+  const uint64_t D = h->cfg.d_c + h->d_r, w = 2 * h->cfg.d_h;
+  if (!make_map(&mc, up.pool, (uint64_t)up.num_pages * kPage, D, D * 2, kPage, Sh::CW) ||
+      !make_map(&mkv, kv, (uint64_t)up.kv_rows * h->cfg.h, w, w * 2, 128, 64))
+    return cudaErrorInvalidValue;
   const int per_sm = 2 * (Sh::SMEM + 1024) <= 227 * 1024 ? 2 : 1;
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = launch_cfg(dim3(h->num_sms * per_sm), dim3(Sh::THREADS), Sh::SMEM, s, true, &attr);
-  return cudaLaunchKernelEx(&cfg, mlra_rows_up_kernel<Sh, true>, h->map_wuk, h->map_wuv, mc, up);
+  return cudaLaunchKernelEx(&cfg, mlra_rows_up_kernel<Sh, true>, h->map_wuk, h->map_wuv, mc, mkv, up);
 }
 
 template <int DBB, int DH, int SUMK>
@@ -381,7 +386,7 @@ cudaError_t launch_up(const mlra_ctx* h, const __nv_bfloat16* o, int tokens, con
   const int grid = (int)(items < (long long)h->num_sms * per_sm ? items : (long long)h->num_sms * per_sm);
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = launch_cfg(dim3(grid), dim3(Sh::THREADS), Sh::SMEM, s, true, &attr);
-  return cudaLaunchKernelEx(&cfg, mlra_rows_up_kernel<Sh>, h->map_wuv, h->map_wuv, mo, up);
+  return cudaLaunchKernelEx(&cfg, mlra_rows_up_kernel<Sh>, h->map_wuv, h->map_wuv, mo, mo, up);
 }
 
 // bf16 absorb for every variant (the E4M3 cache's scales go into the two query scales)
@@ -446,7 +451,6 @@ int run_prefill_heads(mlra_handle h, const void* q, const int32_t* cu, int total
   up.d_c = h->cfg.d_c;
   up.d_r = h->d_r;
   up.pool = static_cast<const __nv_bfloat16*>(pool);
-  up.kv = w.kv;
   up.kr = w.kr;
   RowsCall c = {};
   c.q_pack = static_cast<const __nv_bfloat16*>(q);
@@ -471,8 +475,8 @@ int run_prefill_heads(mlra_handle h, const void* q, const int32_t* cu, int total
   c.rp.tags = tags;
   c.rp.wait_limit_ns = kWaitLimitNs;
   g_use_pdl = true;
-  cudaError_t e = h->d_b == 128 ? launch_expand<128>(h, up, s)
-                : h->d_b == 256 ? launch_expand<256>(h, up, s) : launch_expand<512>(h, up, s);
+  cudaError_t e = h->d_b == 128 ? launch_expand<128>(h, up, w.kv, s)
+                : h->d_b == 256 ? launch_expand<256>(h, up, w.kv, s) : launch_expand<512>(h, up, w.kv, s);
   if (e == cudaSuccess) e = launch_plan<RowsHead>(h, c, w.status, s);
   if (e == cudaSuccess) e = launch_rows<RowsHead>(h, c, s);
   if (e == cudaSuccess) e = launch_merge<RowsHead>(h, c, s);
@@ -489,6 +493,7 @@ int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t*
     return MLRA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(pool) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return MLRA_ERR_INVALID_ARG;
+  if ((long long)(total_q + 127) / 128 * h->cfg.h > 0x7fffffffLL / 2) return MLRA_ERR_UNSUPPORTED;
   if ((long long)num_pages * kPage > 0x7fffffffLL ||
       (h->fp8 && (long long)batch * pt_stride * kPage > 0x7fffffffLL))
     return MLRA_ERR_UNSUPPORTED;
