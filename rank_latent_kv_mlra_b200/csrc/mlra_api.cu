@@ -688,6 +688,7 @@ int mlra_create(const mlra_config* cfg, const void* w_uk, const void* w_uv, mlra
   }
   if (e == cudaSuccess) e = prep_producer();
   if (e == cudaSuccess) e = prep_rows(h->var);
+  if (e == cudaSuccess) e = prep_absorb_plan(h->var);
   if (e == cudaSuccess) e = prep_prefix(h->var, summed);
   if (e != cudaSuccess) {
     delete h;

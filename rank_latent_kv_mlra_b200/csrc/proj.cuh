@@ -73,6 +73,7 @@ struct ProjParams {
   float rope_scale;    // value of a RoPE byte = rope_scale * e4m3(byte)
   float* qfac;         // [B][nsub][np] factor of each head's query terms
   int q_rows_per_sub;  // query rows per (sequence, decode CTA): np, or 2 * np for two terms
+  RowPlanParams rows;  // absorb with PLAN
   // parts of a prefix that sequences share (combine with PREFIX; see rows.cuh)
   PrefixParts prefix;
   int* status;        // cleared by absorb CTA (0, 0); written by the combine kernel
@@ -131,7 +132,9 @@ struct ProjShape {
 // (times scale * log2 e) of each (sequence, head) is multiplied by a power of two 2^E that puts
 // its largest magnitude in [128, 256), and stored as two E4M3 terms (hi: the nearest E4M3
 // value, lo: the nearest to the remainder) in rows prow and np + prow; qfac receives 2^-E.
-template <class Sh, bool F8 = false>
+// PLAN: the first row of blocks makes the split plan of the row attention that follows (its block 0;
+// 3.5 us that would otherwise follow the absorption), batch tiles follow from the second row on.
+template <class Sh, bool F8 = false, bool PLAN = false>
 __global__ void __launch_bounds__(kProjThreads, 1)
     mlra_absorb_kernel(const __grid_constant__ CUtensorMap map_wuk, const __grid_constant__ CUtensorMap map_qc,
                        const __grid_constant__ CUtensorMap map_qr, const ProjParams p) {
@@ -139,6 +142,15 @@ __global__ void __launch_bounds__(kProjThreads, 1)
   static_assert(NT * DB * 2 <= Sh::OFF_QRS, "output staging must not overlap the q^R staging");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   MLRA_TRACE_INIT
+  if (PLAN && blockIdx.y == 0) {
+    if (blockIdx.x != 0) return;
+    grid_dependency_wait();  // the plan's place may be in use by the work before
+    grid_launch_dependents();
+    if (make_row_plan(p.rows, *reinterpret_cast<PlanShared*>(smem_raw)) && threadIdx.x == 0)
+      report_early(p.tags, kTagSeqLen);
+    return;
+  }
+  const int by = blockIdx.y - (PLAN ? 1 : 0);
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* A = smem;
@@ -150,7 +162,7 @@ __global__ void __launch_bounds__(kProjThreads, 1)
   float* stf = reinterpret_cast<float*>(smem + Sh::OFF_STF);  // F8 only: [NT][DB + d_r] fp32
 
   const int head = blockIdx.x;
-  const int n0 = blockIdx.y * NT;
+  const int n0 = by * NT;
   const int warp = warp_id(), lane = lane_id();
   const int qw = DB + p.d_r;
   bool mma_issued = false;  // (warp 0) the MMA went out: its commit is drained at teardown
@@ -178,7 +190,7 @@ __global__ void __launch_bounds__(kProjThreads, 1)
       for (int r0 = 0; r0 < Sh::NMT * 128; r0 += Sh::A1_BOXR)
         tma_load_2d(A + kr * Sh::A1_REG + r0 * Sh::AROWB, &map_wuk, &bars[0], kr * Sh::AW, head * DB + r0, pol);
     grid_dependency_wait();
-    if (blockIdx.x == 0 && blockIdx.y == 0) clear_status_and_tags(p.status, p.tags);
+    if (blockIdx.x == 0 && by == 0) clear_status_and_tags(p.status, p.tags);
     if (tma_q) {
       const int qh = head % p.q_heads;
       for (int kr = 0; kr < Sh::NKR; ++kr)
@@ -277,7 +289,7 @@ __global__ void __launch_bounds__(kProjThreads, 1)
   __syncthreads();
   if (threadIdx.x == 0) MLRA_TRACE_POINT(0, 2);
 
-  const bool stall = p.inject_stall == 2 && blockIdx.x == 1 && blockIdx.y == 0;
+  const bool stall = p.inject_stall == 2 && blockIdx.x == 1 && by == 0;
   if (warp == 0) {
     const bool ok = __all_sync(0xffffffffu, mbar_wait(&bars[0], 0, abort_flag, p.wait_limit_ns));
     if (ok && !stall) {

@@ -96,21 +96,29 @@ __device__ __forceinline__ T block_exclusive_scan(T v, T* scratch, T* total) {
   return (warp_id() > 0 ? before : T(0)) + x - v;
 }
 
-// One CTA. Bounded by latency: a block scan per 1024 token tiles.
-__global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const RowPlanParams p) {
-  __shared__ int base[kMaxSeqs + 1];  // first token tile of each sequence
-  __shared__ long long scratch[32];
-  __shared__ int scratch_i[32];
-  __shared__ int flags[2];  // bad lengths; tiles without a key
-  __shared__ long long starts[kPlanStarts];
+// Shared memory of the planning block.
+struct PlanShared {
+  int base[kMaxSeqs + 1];   // first token tile of each sequence
+  long long starts[kPlanStarts];
+  long long scratch[32];
+  int scratch_i[32];
+  int flags[2];             // bad lengths; tiles without a key
+};
+
+// The plan, by one block (a multiple of 32 threads). Returns the bad lengths found. Bound by
+// latency: a block scan for as many token tiles as there are threads.
+__device__ __forceinline__ int make_row_plan(const RowPlanParams& p, PlanShared& sh) {
+  int* const base = sh.base;
+  long long* const starts = sh.starts;
+  long long* const scratch = sh.scratch;
+  int* const scratch_i = sh.scratch_i;
+  int* const flags = sh.flags;
+  const int threads = blockDim.x;
   if (threadIdx.x < 2) flags[threadIdx.x] = 0;
   __syncthreads();
-  grid_launch_dependents();
-  // This kernel's inputs were there before the call and its outputs are read by later kernels of
-  // the call only; the kernel in front of it (absorb) waited for the work before the call.
   int bad = 0;  // 1: a length outside its table row; 2: cu not ascending within [0, total_q]
   int running = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < p.batch; b0 += threads) {
     const int b = b0 + threadIdx.x;
     int tiles = 0;
     if (b < p.batch) {
@@ -126,15 +134,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const R
   }
   if (bad) atomicOr(&flags[0], bad);
   if (p.plan.tok != nullptr)  // tokens of no sequence
-    for (int i = threadIdx.x; i < p.total_q; i += kPlanThreads) p.plan.tok[i] = make_int4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < p.total_q; i += threads) p.plan.tok[i] = make_int4(0, 0, 0, 0);
   __syncthreads();
   // packed offsets that do not ascend leave no work at all
   const int tiles = (flags[0] & 2) ? 0 : running;
   if (threadIdx.x == 0) base[p.batch] = running;
   __syncthreads();
-  for (int b = threadIdx.x; b <= p.batch; b += kPlanThreads) p.plan.base[b] = base[b];
+  for (int b = threadIdx.x; b <= p.batch; b += threads) p.plan.base[b] = base[b];
   long long pos = 0;
-  for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
+  for (int i0 = 0; i0 < tiles; i0 += threads) {
     const int i = i0 + threadIdx.x;
     long long cost = 0;
     TokenTile t = {0, 0, 0, 0};
@@ -184,7 +192,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const R
   }
   __syncthreads();
   // where each CTA begins, so that it need not search
-  for (int c = threadIdx.x; c < p.ctas; c += kPlanThreads) {
+  for (int c = threadIdx.x; c < p.ctas; c += threads) {
     const Stretch s = stretch_of(pos, c, p.ctas);
     if (s.lo >= s.hi) continue;
     const long long* st = tiles < kPlanStarts ? starts : p.plan.start;
@@ -200,8 +208,18 @@ __global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const R
     p.plan.first[3 * c + 1] = make_int4((int)nx, (int)(nx >> 32), 0, 0);
     p.plan.first[3 * c + 2] = make_int4(t.b, t.tok0, t.ntok, t.lim0);
   }
-  grid_dependency_wait();  // the absorb kernel clears the status word
-  if (threadIdx.x == 0 && flags[0]) set_status(p.status, kErrSeqLen);
+  return flags[0];
+}
+
+// As a kernel of its own (behind the expansion, which clears the status word).
+__global__ void __launch_bounds__(kPlanThreads, 1) mlra_rows_plan_kernel(const RowPlanParams p) {
+  __shared__ PlanShared sh;
+  grid_launch_dependents();
+  // Its inputs were there before the call and its outputs are read by later kernels of the call only;
+  // the kernel in front of it waited for the work before the call.
+  const int bad = make_row_plan(p, sh);
+  grid_dependency_wait();
+  if (threadIdx.x == 0 && bad) set_status(p.status, kErrSeqLen);
 }
 
 // One unit's key tiles that lie in a stretch.

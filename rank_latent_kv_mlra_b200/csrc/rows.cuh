@@ -883,7 +883,12 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) fold_early(p.tags, p.status);
+    if (blockIdx.x == 0) {
+      fold_early(p.tags, p.status);
+      // a bad length is the cause of the pages it leads to, whichever was seen first
+      if (*reinterpret_cast<volatile unsigned*>(p.tags.words + kTagSeqLen) == p.tags.tag)
+        atomicCAS(p.status, kErrPageOob, kErrSeqLen);
+    }
     if (*abort_flag) set_status(p.status, kErrTimeout);
     if (*drain_err) force_status(p.status, kErrDrain);
   }

@@ -270,7 +270,7 @@ struct RowsCall {
 };
 
 template <class Sh>
-cudaError_t launch_plan(const mlra_ctx* h, const RowsCall& c, int* status, cudaStream_t s) {
+RowPlanParams plan_params(const mlra_ctx* h, const RowsCall& c, int* status) {
   RowPlanParams p = {};
   p.cu = c.cu;
   p.lens = c.lens;
@@ -284,9 +284,13 @@ cudaError_t launch_plan(const mlra_ctx* h, const RowsCall& c, int* status, cudaS
   p.tile_tokens = Sh::NQ * (128 / (Sh::SPLIT ? 1 : heads_tile_of(h)));
   p.key_tile = Sh::KT;
   p.units = Sh::SPLIT ? h->cfg.h : h->nsub * Sh::HALVES;
+  return p;
+}
+template <class Sh>
+cudaError_t launch_plan(const mlra_ctx* h, const RowsCall& c, int* status, cudaStream_t s) {
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = launch_cfg(dim3(1), dim3(kPlanThreads), 0, s, true, &attr);
-  return cudaLaunchKernelEx(&cfg, mlra_rows_plan_kernel, p);
+  return cudaLaunchKernelEx(&cfg, mlra_rows_plan_kernel, plan_params<Sh>(h, c, status));
 }
 
 template <class Sh>
@@ -389,13 +393,64 @@ cudaError_t launch_up(const mlra_ctx* h, const __nv_bfloat16* o, int tokens, con
   return cudaLaunchKernelEx(&cfg, mlra_rows_up_kernel<Sh>, h->map_wuv, h->map_wuv, mo, mo, up);
 }
 
-// bf16 absorb for every variant (the E4M3 cache's scales go into the two query scales)
+// bf16 absorb for every variant, with the split plan in its first row of blocks (an E4M3 cache's
+// scales are in the two query scales).
+template <int DB, int DH, int NT>
+constexpr int plan_smem() {
+  return ProjShape<DB, DH, NT>::SMEM1 > (int)sizeof(PlanShared) ? ProjShape<DB, DH, NT>::SMEM1 : (int)sizeof(PlanShared);
+}
+template <int DB, int DH>
+cudaError_t prep_absorb_rows() {
+  cudaError_t e = prep_kernel(mlra_absorb_kernel<ProjShape<DB, DH, 16>, false, true>, plan_smem<DB, DH, 16>());
+  if (e == cudaSuccess) e = prep_kernel(mlra_absorb_kernel<ProjShape<DB, DH, 32>, false, true>, plan_smem<DB, DH, 32>());
+  if (e == cudaSuccess) e = prep_kernel(mlra_absorb_kernel<ProjShape<DB, DH, 64>, false, true>, plan_smem<DB, DH, 64>());
+  if constexpr (max_nt<DB>() >= 128)
+    if (e == cudaSuccess)
+      e = prep_kernel(mlra_absorb_kernel<ProjShape<DB, DH, 128>, false, true>, plan_smem<DB, DH, 128>());
+  return e;
+}
+template <int DB, int DH, int NT>
+cudaError_t launch_absorb_rows(const mlra_ctx* h, const ProjParams& pp, int tokens, cudaStream_t s) {
+  using S = ProjShape<DB, DH, NT>;
+  CUtensorMap mqc, mqr;
+  std::memset(&mqc, 0, sizeof(mqc));
+  std::memset(&mqr, 0, sizeof(mqr));
+  if (!pp.q_f32) {
+    const uint64_t cols = (uint64_t)DH + h->d_r;
+    if (!make_q_map(&mqc, pp.q, tokens, h->cfg.h, cols, S::AW, NT, swizzle_for(S::AROWB)) ||
+        !make_q_map(&mqr, pp.q, tokens, h->cfg.h, cols, h->d_r, NT, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
+  }
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t c = launch_cfg(dim3(h->vh, (tokens + NT - 1) / NT + 1), dim3(kProjThreads), plan_smem<DB, DH, NT>(),
+                                    s, true, &attr);
+  return cudaLaunchKernelEx(&c, mlra_absorb_kernel<S, false, true>, h->map_wuk, mqc, mqr, pp);
+}
+template <int DB, int DH>
+cudaError_t dispatch_absorb_plan(const mlra_ctx* h, const ProjParams& pp, int tokens, cudaStream_t s) {
+  switch (nt_for(tokens, max_nt<DB>())) {
+    case 16: return launch_absorb_rows<DB, DH, 16>(h, pp, tokens, s);
+    case 32: return launch_absorb_rows<DB, DH, 32>(h, pp, tokens, s);
+    case 64: return launch_absorb_rows<DB, DH, 64>(h, pp, tokens, s);
+    default:
+      if constexpr (max_nt<DB>() >= 128) return launch_absorb_rows<DB, DH, 128>(h, pp, tokens, s);
+      return cudaErrorInvalidValue;
+  }
+}
 cudaError_t dispatch_absorb_rows(const mlra_ctx* h, const ProjParams& pp, int tokens, cudaStream_t s) {
   switch (h->var) {
-    case kTiny: return dispatch_absorb<32, 32>(h, pp, tokens, s);
-    case kMlra2: case kMlra2Sum: return dispatch_absorb<256, 128>(h, pp, tokens, s);
-    case kMla: return dispatch_absorb<512, 128>(h, pp, tokens, s);
-    default: return dispatch_absorb<128, 128>(h, pp, tokens, s);
+    case kTiny: return dispatch_absorb_plan<32, 32>(h, pp, tokens, s);
+    case kMlra2: case kMlra2Sum: return dispatch_absorb_plan<256, 128>(h, pp, tokens, s);
+    case kMla: return dispatch_absorb_plan<512, 128>(h, pp, tokens, s);
+    default: return dispatch_absorb_plan<128, 128>(h, pp, tokens, s);
+  }
+}
+cudaError_t prep_absorb_plan(Variant v) {
+  switch (v) {
+    case kTiny: return prep_absorb_rows<32, 32>();
+    case kMlra2: case kMlra2Sum: return prep_absorb_rows<256, 128>();
+    case kMla: return prep_absorb_rows<512, 128>();
+    default: return prep_absorb_rows<128, 128>();
   }
 }
 
@@ -536,6 +591,7 @@ int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t*
   c.rp.tags = tags;
   c.rp.wait_limit_ns = kWaitLimitNs;
 
+  pp.rows = with_rows(h->var, [&](auto sh) { return plan_params<decltype(sh)>(h, c, w.status); });
   g_use_pdl = true;
   cudaError_t e = dispatch_absorb_rows(h, pp, total_q, s);
   if (e == cudaSuccess && h->fp8) {
@@ -547,8 +603,7 @@ int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t*
   if (e == cudaSuccess)
     e = with_rows(h->var, [&](auto sh) {
       using Sh = decltype(sh);
-      cudaError_t r = launch_plan<Sh>(h, c, w.status, s);
-      if (r == cudaSuccess) r = launch_rows<Sh>(h, c, s);
+      const cudaError_t r = launch_rows<Sh>(h, c, s);
       return r == cudaSuccess ? launch_merge<Sh>(h, c, s) : r;
     });
   if (e == cudaSuccess) {
@@ -679,10 +734,9 @@ int run_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const vo
       !make_map(&mqr, w.dec.q_pack, qrows, qw, qw * 2, dp.q_rows, rw))
     return MLRA_ERR_CUDA;
 
+  pp.rows = with_rows(h->var, [&](auto sh) { return plan_params<decltype(sh)>(h, c, w.dec.status); });
   g_use_pdl = true;
   cudaError_t e = dispatch_absorb_rows(h, pp, batch, s);
-  if (e == cudaSuccess)
-    e = with_rows(h->var, [&](auto sh) { return launch_plan<decltype(sh)>(h, c, w.dec.status, s); });
   if (e == cudaSuccess) switch (h->var) {
       case kTiny: e = launch_decode<DecTiny>(h, mc, mr, mqc, mqr, dp, s); break;
       case kMlra4: e = launch_decode<DecMlra4>(h, mc, mr, mqc, mqr, dp, s); break;
