@@ -455,7 +455,9 @@ __global__ void __launch_bounds__(kProjThreads, 1)
 // virtual heads j*out_heads + head (latent block j), lays them side by side along K
 // (DB = SUMK * block width) and multiplies by the SUMK stacked W^UV matrices in one GEMM, so
 // the sum over blocks happens in the tensor core's accumulator; out_scale applies alpha_attn.
-// PREFIX: after a sequence's own partials come the parts of the prefix it shares with others.
+// PREFIX: after a sequence's own partials come the parts of the prefix it shares with others. Without
+// seq_lens there are no own partials: the rows are a prompt's tokens, those behind the last sequence
+// stay as they were.
 template <class Sh, bool LATENT_ONLY, int SUMK = 1, bool PREFIX = false>
 __global__ void __launch_bounds__(kProjThreads, 1)
     mlra_uproj_kernel(const __grid_constant__ CUtensorMap map_wuv, const ProjParams p) {
@@ -514,9 +516,12 @@ __global__ void __launch_bounds__(kProjThreads, 1)
   // a block-wide scan into pref[].
   int err = 0;
   WarpPlan wp;
-  const bool warp_plan = warp_plan_load(p.seq_lens, p.batch, cap_len, wp, &err);
+  const bool no_own = PREFIX && p.seq_lens == nullptr;
+  const bool warp_plan = no_own || warp_plan_load(p.seq_lens, p.batch, cap_len, wp, &err);
   int T;
-  if (warp_plan) {
+  if (no_own) {
+    T = 0;
+  } else if (warp_plan) {
     T = wp.total;
   } else {
     T = block_total_tiles(p.seq_lens, p.batch, cap_len, scratch, &err);
@@ -541,6 +546,8 @@ __global__ void __launch_bounds__(kProjThreads, 1)
   grid_launch_dependents();
   if (threadIdx.x == 0) MLRA_TRACE_POINT(2, 2);
 
+  const int rows_out = no_own ? min(p.batch, __ldg(p.prefix.plan.hdr + 1)) : p.batch;
+
   // merge the split partials of each (sequence, head) and stage o~ as bf16 (K-major).
   // Warp w takes batch rows w*RB .. w*RB+RB-1 (then + NW*RB ...) and issues every load of a
   // round (the rows' lse values and partial vectors, up to SB segments each) before using
@@ -561,7 +568,7 @@ __global__ void __launch_bounds__(kProjThreads, 1)
       const int bl = r0 + rb, b = n0 + bl;
       c0[rb] = 0;
       nsg[rb] = 0;
-      if (bl < NT && b < p.batch) {
+      if (!no_own && bl < NT && b < p.batch) {
         int tb, pb;
         if (warp_plan) {
           pb = warp_plan_start(wp, b, &tb);
@@ -659,6 +666,12 @@ __global__ void __launch_bounds__(kProjThreads, 1)
         float m_new = mx[rb];
 #pragma unroll
         for (int si = 0; si < SB; ++si) m_new = fmaxf(m_new, lv[rb][si]);
+        if constexpr (PREFIX) {
+          // a part that is NaN makes the row NaN (fmaxf passes it over)
+#pragma unroll
+          for (int si = 0; si < SB; ++si)
+            if (lv[rb][si] != lv[rb][si]) sum[rb] = NAN;
+        }
         if (m_new == -INFINITY) continue;
         // ex2.approx: these weights lie in [0, 1] and the merge is fp32 (relative error ~2^-22)
         const float sc = fast_exp2(mx[rb] - m_new);  // 0 when mx was -inf
@@ -681,10 +694,11 @@ __global__ void __launch_bounds__(kProjThreads, 1)
       const int bl = r0 + rb, b = n0 + bl;
       if (bl >= NT) continue;
       // sum >= 1 (the largest segment's own weight is 1): div.approx is within 2 ulp
-      const float inv = sum[rb] > 0.f ? __fdividef(1.f, sum[rb]) : 0.f;
+      float inv = sum[rb] > 0.f ? __fdividef(1.f, sum[rb]) : 0.f;
+      if (PREFIX && sum[rb] != sum[rb]) inv = NAN;
 #pragma unroll
       for (int e = 0; e < PER; ++e) acc[rb][e] *= inv;
-      if (b < p.batch && f0 == 0 && p.lse_out)  // one lane per (virtual) head
+      if (b < rows_out && f0 == 0 && p.lse_out)  // one lane per (virtual) head
         p.lse_out[(size_t)b * p.h + vhead] =
             nsg[rb] + npx[rb] > 0 ? (mx[rb] + __log2f(sum[rb])) * kLn2 : -INFINITY;
       if constexpr (LATENT_ONLY) {
@@ -774,7 +788,7 @@ __global__ void __launch_bounds__(kProjThreads, 1)
       for (int idx = threadIdx.x; idx < NT * chunks; idx += kProjThreads) {
         const int n = idx / chunks, c = idx % chunks;
         const int b = n0 + n;
-        if (b < p.batch)
+        if (b < rows_out)
           *reinterpret_cast<uint4*>(static_cast<char*>(p.out) + (((size_t)b * p.out_heads + head) * DH) * esz + c * 16) =
               *reinterpret_cast<const uint4*>(A + (size_t)n * DH * esz + c * 16);
       }

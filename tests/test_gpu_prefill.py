@@ -137,6 +137,15 @@ CASES = {
     # name: (workload, new tokens, older tokens)
     "one_token": (MLRA4, [1], [0]),
     "one_token_long": (MLRA4, [1], [1000]),
+    # few tokens (merged by the decode step's combine), each kind of handle
+    "few_mla": (MLA, [3, 20], [700, 40]),
+    "few_mlra2": (MLRA2, [3, 20], [700, 40]),
+    "few_tiny": (TINY, [3, 20, 0, 9], [700, 40, 9, 0]),
+    "few_e4m3": (E4M3, [3, 20], [700, 40]),
+    "few_sum4": (SUM4, [3, 20], [700, 40]),
+    "few_sum2": (SUM2, [3, 20], [700, 40]),
+    "few_32": (MLRA4, [2, 30], [700, 40]),
+    "not_few_33": (MLRA4, [3, 30], [700, 40]),
     "tile_edges": (MLRA4, [3, 4, 5, 8, 9, 127, 128, 129], [0, 64, 63, 0, 65, 1, 0, 127]),
     "empty_sequences": (MLRA4, [0, 7, 0, 0, 130, 0], [0, 0, 300, 0, 5, 64]),
     "ragged": (MLRA4, [333, 1, 64, 511, 20], [0, 0, 0, 77, 700]),
@@ -293,6 +302,28 @@ def test_a_bad_cached_row_reaches_only_the_tokens_that_see_it(value, form):
     assert status == 0
     assert torch.equal(out[:100], clean[:100]) and torch.equal(lse[:100], clean_lse[:100])
     assert out[100:].isnan().all()
+
+
+@pytest.mark.parametrize("n,past", [(30, 0), (30, 900)])
+def test_a_bad_cached_row_with_few_tokens(n, past):
+    """The same for a call of few tokens, whose parts the decode step's combine merges."""
+    w, inp = make(MLRA4, [n], [past], seed=18, form="absorbed")
+    hdl = handle(w, inp)
+    clean, clean_lse, _ = run(hdl, w, inp)
+    inp["pool"][int(inp["page_table"][0, (past + 20) // 64]), (past + 20) % 64] = float("nan")
+    out, lse, status = run(hdl, w, inp)
+    assert status == 0
+    assert torch.equal(out[:20], clean[:20]) and torch.equal(lse[:20], clean_lse[:20])
+    assert out[20:].isnan().all() and lse[20:].isnan().all()
+
+
+@BOTH
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_few_rows_behind_the_last_sequence_stay(form, dtype):
+    w, inp = make(MLRA4, [10, 11], [0, 7], seed=19, behind=11, form=form if form == "absorbed" else None)
+    out, lse, status = run(handle(w, inp), w, inp, dtype)
+    check(w, inp, out, lse, status, "padded batch")
+    assert out[21:].isnan().all() and lse[21:].isnan().all()
 
 
 @BOTH
