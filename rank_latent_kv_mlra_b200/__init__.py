@@ -352,12 +352,13 @@ def _call(name, dev, stream, *args):
     """Calls the library's `name` on `dev`, with the stream (None: the device's current one) last."""
     fn = getattr(load_library(), name)
     raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, raw)
-    _check(rc, name)
+    if rc != 0:
+        raise MlraError(rc, name)
 
 
 def _new_workspace(size: int, dev, stream):
@@ -469,31 +470,42 @@ def mlra_pages_workspace_size(handle: Handle, num_pages: int, batch: int) -> int
 
 
 def _pages_call(name, handle, pool, refs, page_table, seq_lens, requests, workspace, stream, used=None):
-    """One page operator: checks, workspace, call. `pool` None and `requests` () where it has none."""
-    _require(refs, "refs", torch.int32)
-    _tables(page_table, seq_lens, ("page_table", "seq_lens"))
-    if refs.dim() != 1:
-        raise ValueError("refs must be [num_pages]")
-    P, (B, stride) = refs.shape[0], page_table.shape
+    """One page operator: checks, workspace, call. `pool` None and `requests` () where it has none.
+    (A turn makes several of these calls on little data: they are kept short.)"""
+    dev = refs.device
+    for what, t in zip(("refs", "page_table", "seq_lens", "requests", "requests"),
+                       (refs, page_table, seq_lens, *requests)):
+        if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous() or t.device != dev:
+            _require(t, what, torch.int32)
+            raise ValueError(f"the tensors of {name} must be on one device")
+    P, (B, stride) = refs.numel(), page_table.shape
+    if refs.dim() != 1 or seq_lens.shape != (B,):
+        raise ValueError("refs must be [num_pages], page_table [rows][stride], seq_lens [rows]")
+    n = requests[0].numel() if requests else 0
+    for t in requests:
+        if t.dim() != 1 or t.numel() != n:
+            raise ValueError("requests must be vectors of one length")
+    if workspace is None:
+        workspace = _new_workspace(mlra_pages_workspace_size(handle, P, B), dev, stream)
+    _require(workspace, "workspace")
+    _one_device(f"the tensors of {name}", refs, workspace, pool, used)
+    args = [handle.ptr]
     if pool is not None:
         _require(pool, "pool", _pool_dtype(handle))
         cfg = handle.cfg
         if pool.shape != (P, cfg.page_size, cfg.d_c + cfg.d_rope):
             raise ValueError("pool must be [num_pages][page_size][d_c + d_rope]")
-    if used is not None:
-        _require(used, "used", torch.int32)
+        args.append(pool.data_ptr())
+    args += (refs.data_ptr(), P, page_table.data_ptr(), stride, B, seq_lens.data_ptr())
     for t in requests:
-        _require(t, "requests", torch.int32)
-        if t.dim() != 1 or t.shape != requests[0].shape:
-            raise ValueError("requests must be vectors of one length")
-    if workspace is None:
-        workspace = _new_workspace(mlra_pages_workspace_size(handle, P, B), refs.device, stream)
-    _require(workspace, "workspace")
-    dev = _one_device(f"the tensors of {name}", refs, page_table, seq_lens, workspace, pool, used, *requests)
-    lead = (handle.ptr,) if pool is None else (handle.ptr, pool.data_ptr())
-    tail = (*(t.data_ptr() for t in requests), requests[0].shape[0]) if requests else (_addr(used),)
-    _call(name, dev, stream, *lead, refs.data_ptr(), P, page_table.data_ptr(), stride, B, seq_lens.data_ptr(), *tail,
-          workspace.data_ptr(), workspace.nbytes)
+        args.append(t.data_ptr())
+    if requests:
+        args.append(n)
+    else:
+        if used is not None:
+            _require(used, "used", torch.int32)
+        args.append(_addr(used))
+    _call(name, dev, stream, *args, workspace.data_ptr(), workspace.nbytes)
     return workspace
 
 
