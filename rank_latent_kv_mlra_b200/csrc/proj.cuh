@@ -32,7 +32,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // in the slots of the CTAs that worked on them.
 struct PrefixParts {
   RowPlan plan;
-  int ctas, units, halves, chunks, heads_tile, tok_tile, key_tile, rows, dv;
+  int halves, chunks, heads_tile, tok_tile, rows, dv;
   const float* o_dense;   // [batch][h][DB]
   const float* lse_dense; // [batch][h] log2
   const float* part_o;    // [2 * ctas][rows][dv]

@@ -497,7 +497,6 @@ bool rows_sizes_ok(int total_q, int batch, int pt_stride) {
 PrefixParts prefix_parts(const mlra_ctx* h, const RowsWorkspace& w, const float* o, const float* lse) {
   PrefixParts pre = {};
   pre.plan = w.plan;
-  pre.ctas = h->num_sms;
   pre.chunks = h->chunks;
   pre.heads_tile = heads_tile_of(h);
   pre.tok_tile = 128 / pre.heads_tile;
@@ -507,9 +506,7 @@ PrefixParts prefix_parts(const mlra_ctx* h, const RowsWorkspace& w, const float*
   pre.part_lse = w.part_lse;
   with_rows(h->var, [&](auto sh) {
     using Sh = decltype(sh);
-    pre.units = h->nsub * Sh::HALVES;
     pre.halves = Sh::HALVES;
-    pre.key_tile = Sh::KT;
     pre.rows = Sh::ROWS;
     pre.dv = Sh::DV;
     return 0;
