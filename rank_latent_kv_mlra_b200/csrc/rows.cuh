@@ -888,6 +888,8 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       // a bad length is the cause of the pages it leads to, whichever was seen first
       if (*reinterpret_cast<volatile unsigned*>(p.tags.words + kTagSeqLen) == p.tags.tag)
         atomicCAS(p.status, kErrPageOob, kErrSeqLen);
+      // a replayed graph comes with the same tag: what this call found must not be there for the next
+      for (int k = 0; k < 4; ++k) atomicCAS(p.tags.words + k, p.tags.tag, 0u);
     }
     if (*abort_flag) set_status(p.status, kErrTimeout);
     if (*drain_err) force_status(p.status, kErrDrain);

@@ -421,3 +421,35 @@ def test_status_of_bad_lengths_and_pages(form):
     out, _, status = run(hdl, w, dict(inp, page_table=pt))
     assert status == -4
     assert torch.equal(run(hdl, w, inp)[0], good)
+
+
+@BOTH
+def test_a_replayed_graph_does_not_keep_an_earlier_status(form):
+    """Bad lengths and pages in one replay are reported by that replay alone."""
+    w, inp = make(MLRA4, [33, 90], [10, 0], seed=15, form=form)
+    hdl = handle(w, inp)
+    out = torch.empty(123, w.h, w.d_h, device="cuda")
+    ws = torch.empty(M.mlra_prefill_workspace_size(hdl, 123, 2, inp["page_table"].shape[1]), dtype=torch.uint8,
+                     device="cuda")
+    args = (inp["q"], inp["cu"], inp["pool"], inp["page_table"], inp["seq_lens"], out)
+    M.mlra_prefill(hdl, *args, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.mlra_prefill(hdl, *args, workspace=ws)
+
+    def replay():
+        graph.replay()
+        return int(ws[:4].view(torch.int32)[0])
+
+    assert replay() == 0
+    good = out.clone()
+    inp["seq_lens"][1] = 10 ** 6
+    assert replay() == -7
+    inp["seq_lens"][1] = 90
+    assert replay() == 0 and torch.equal(out, good)
+    page = int(inp["page_table"][0, 0])
+    inp["page_table"][0, 0] = inp["pool"].shape[0]
+    assert replay() == -4
+    inp["page_table"][0, 0] = page
+    assert replay() == 0 and torch.equal(out, good)

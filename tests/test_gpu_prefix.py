@@ -227,3 +227,31 @@ def test_status_of_bad_lengths_offsets_and_pages():
     pt[1, 1] = -3
     assert run(hdl, w, dict(inp, pre_table=pt))[2] == -4
     assert torch.equal(run(hdl, w, inp)[0], good)
+
+
+def test_a_replayed_graph_does_not_keep_an_earlier_status():
+    """Bad lengths and offsets in one replay are reported by that replay alone."""
+    w, inp = make(MLRA4, [0, 2, 5], [600, 200], [10, 0, 64, 100, 3], seed=10)
+    hdl = handle(w, inp)
+    out = torch.empty(5, w.h, w.d_h, device="cuda")
+    ws = torch.empty(M.mlra_decode_prefix_workspace_size(hdl, 5, 2), dtype=torch.uint8, device="cuda")
+    args = (inp["q"], inp["pool"], inp["pre_table"], inp["pre_lens"], inp["offsets"], inp["suf_table"],
+            inp["suf_lens"], out)
+    M.mlra_decode_prefix(hdl, *args, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.mlra_decode_prefix(hdl, *args, workspace=ws)
+
+    def replay():
+        graph.replay()
+        return int(ws[:4].view(torch.int32)[0])
+
+    assert replay() == 0
+    good = out.clone()
+    for name, at, wrong in (("pre_lens", 1, 10 ** 6), ("offsets", 1, 6), ("suf_lens", 2, -1)):
+        right = int(inp[name][at])
+        inp[name][at] = wrong
+        assert replay() == -7
+        inp[name][at] = right
+        assert replay() == 0 and torch.equal(out, good)
