@@ -233,9 +233,11 @@ int mlra_project_append(mlra_handle h, const void* x, int d_model, const void* w
                         const int32_t* positions, void* pool, int num_pages, const int32_t* page_table,
                         int pt_stride, int batch, void* workspace, size_t ws_bytes, void* stream);
 
-/* Bytes of device workspace mlra_prefill needs (host output): about 80 KB a query token with 128
- * heads of 128 (packed query and latent result), plus a fixed part of some 40 MB; with an E4M3
- * cache also the bf16 form of batch * pt_stride pages. */
+/* Bytes of device workspace mlra_prefill needs for a call of these sizes (host output): about 80 KB a
+ * query token with 128 heads of 128 (packed query and latent result), plus a fixed part of some
+ * 40 MB; with an E4M3 cache also the bf16 form of batch * pt_stride pages. A call whose page table
+ * holds at most four times its query tokens (whole prompts) keeps every head's keys and values
+ * instead, 64 KB a row of the table's capacity, so that a narrower table may need more than a wide one. */
 int mlra_prefill_workspace_size(mlra_handle h, int total_q, int batch, int pt_stride, size_t* bytes);
 
 /* Causal attention of the query tokens of packed sequences (whole prompts, or the next tokens of
@@ -260,9 +262,12 @@ int mlra_prefill_workspace_size(mlra_handle h, int total_q, int batch, int pt_st
  *   workspace  device, >= mlra_prefill_workspace_size bytes, 256-byte aligned; its first 4 bytes
  *              become this call's status word.
  * A row of the cache that holds NaN or infinities reaches only the tokens that attend to it.
- * Launches five kernels on `stream` (six with an E4M3 cache), chained by programmatic dependent
- * launch: query absorption, the split plan, the attention, the merge of split results and the
- * up-projection. The result does not depend on timing. batch <= 4096. */
+ * Launches four kernels on `stream`, chained by programmatic dependent launch. Absorbed form: query
+ * absorption with the split plan, (E4M3 cache: its pages as bf16,) the attention, the merge of split
+ * results, up-projection; up to 32 tokens at d_b <= 128 the last two are one. Whole prompts at d_h = 128
+ * (bf16 query and cache, blocks not summed; see the workspace): every head's keys and values from the
+ * cached rows, the split plan, the attention, the merge. For given sizes the result does not depend on
+ * timing; the two forms round differently. batch <= 4096. */
 int mlra_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t* cu_seqlens, int total_q,
                  const void* pool, int num_pages, const int32_t* page_table, int pt_stride, const int32_t* seq_lens,
                  int batch, void* out, mlra_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes,

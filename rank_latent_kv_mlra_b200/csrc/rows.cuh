@@ -12,7 +12,8 @@
 // stretch [c * quota, (c + 1) * quota) of all the units' costs laid end to end. A unit that lies in
 // one stretch is finished there; one that is cut leaves normalised fp32 partials with their
 // log-sum-exp, merged afterwards in a fixed order. The split needs lengths that only the device
-// has, so a one-CTA kernel (mlra_rows_plan_kernel) lays the units out.
+// has, so one block lays the units out in front of it: of the absorb kernel, or (per-head form) a
+// kernel of one block.
 //
 // What bounds it: a 128 x 128 tile at d_b = 128, d_rope = 64 is 12 + 8 tcgen05 MMAs of 64 clocks
 // (1280; the scores' MMAs, both operands from shared memory at N = 128, measure 85 each) against

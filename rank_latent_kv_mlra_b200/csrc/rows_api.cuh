@@ -690,7 +690,8 @@ int run_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const vo
       !workspace)
     return MLRA_ERR_INVALID_ARG;
   if (h->fp8) return MLRA_ERR_UNSUPPORTED;
-  if (!rows_sizes_ok(batch, groups, prefix_stride) || batch <= 0 || batch > 4096 || num_pages <= 0 || pt_stride <= 0)
+  if (!rows_sizes_ok(batch, groups, prefix_stride) || !rows_sizes_ok(batch, batch, pt_stride) || batch <= 0 ||
+      num_pages <= 0)
     return MLRA_ERR_INVALID_ARG;
   if ((q_dtype != MLRA_F32 && q_dtype != MLRA_BF16) || (out_dtype != MLRA_F32 && out_dtype != MLRA_BF16))
     return MLRA_ERR_INVALID_ARG;

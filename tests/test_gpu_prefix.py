@@ -2,6 +2,8 @@
 definition: each sequence attends to its group's prefix rows, then to its own. Same tolerances as
 the decode step (tests/gpu_util.py): the roundings are the same (absorbed query, probabilities,
 merged latent result)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -255,3 +257,15 @@ def test_a_replayed_graph_does_not_keep_an_earlier_status():
         assert replay() == -7
         inp[name][at] = right
         assert replay() == 0 and torch.equal(out, good)
+
+
+def test_tables_wider_than_lengths_can_be_are_refused():
+    """A page table whose capacity passes a 32-bit length (refused before anything is read)."""
+    w, inp = make(MLRA4, [0, 2], [70], [10, 0], seed=11)
+    hdl = handle(w, inp)
+    lib, P = M.load_library(), ctypes.c_void_p
+    call = lambda pre_stride, stride: lib.mlra_decode_prefix(
+        hdl.ptr, P(16), 1, P(16), 4, P(16), pre_stride, P(16), P(16), 1, P(16), stride, P(16), 2, P(16), 1, None, P(256),
+        1, None)
+    assert call(2 ** 25, 1) == -1 and call(1, 2 ** 25) == -1
+    assert call(1, 1) == -6  # (these sizes alone: the workspace is too small)
