@@ -29,7 +29,8 @@ constexpr int kProjThreads = 512;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Where the attention over shared prefixes left its results: whole units in dense rows, cut ones
-// in the slots of the CTAs that worked on them.
+// in the slots of the CTAs that worked on them. Records and dense rows of the tokens' own rows, where
+// that kernel attended to them as well, come behind the prefix's.
 struct PrefixParts {
   RowPlan plan;
   int halves, chunks, heads_tile, tok_tile, rows, dv;
@@ -455,10 +456,12 @@ __global__ void __launch_bounds__(kProjThreads, 1)
 // virtual heads j*out_heads + head (latent block j), lays them side by side along K
 // (DB = SUMK * block width) and multiplies by the SUMK stacked W^UV matrices in one GEMM, so
 // the sum over blocks happens in the tensor core's accumulator; out_scale applies alpha_attn.
-// PREFIX: after a sequence's own partials come the parts of the prefix it shares with others. Without
+// PREFIX: after a sequence's own partials come the parts of the prefix it shares with others; 2: and
+// those of its own rows, where the same kernel attended to them (one more record a row; drafted tokens,
+// which have none, took 30.3 us in place of 28.9 with it). Without
 // seq_lens there are no own partials: the rows are a prompt's tokens, those behind the last sequence
 // stay as they were.
-template <class Sh, bool LATENT_ONLY, int SUMK = 1, bool PREFIX = false>
+template <class Sh, bool LATENT_ONLY, int SUMK = 1, int PREFIX = 0>
 __global__ void __launch_bounds__(kProjThreads, 1)
     mlra_uproj_kernel(const __grid_constant__ CUtensorMap map_wuv, const ProjParams p) {
   constexpr int DB = Sh::DB, DH = Sh::DH, NT = Sh::NT;
@@ -582,18 +585,20 @@ __global__ void __launch_bounds__(kProjThreads, 1)
         }
       }
     }
-    // the prefix's parts: CTAs px0 .. px0 + npx - 1 (npx = 0: none, 1 with px0 < 0: a whole unit)
-    int px0[RB], npx[RB], prow[RB];
+    // the prefix's parts [0] and the own rows' [1]: CTAs px0 .. px0 + npx - 1 (npx = 0: none, 1 with
+    // px0 < 0: a whole unit)
+    constexpr int KP = PREFIX == 2 ? 2 : 1;
+    int px0[RB][KP], npx[RB][KP], prow[RB][KP];
     if constexpr (PREFIX) {
       const PrefixParts& pp = p.prefix;
       const int4 h1 = __ldg(reinterpret_cast<const int4*>(pp.plan.hdr) + 1);
       const long long pquota = join64(h1.x, h1.y);
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        const int bl = r0 + rb, b = n0 + bl;
-        px0[rb] = -1;
-        npx[rb] = prow[rb] = 0;
-        const int4 rec = bl < NT && b < p.batch ? __ldg(pp.plan.tok + b) : make_int4(0, 0, 0, 0);
+      for (int i = 0; i < KP * RB; ++i) {
+        const int rb = i / KP, k = i % KP, bl = r0 + rb, b = n0 + bl;
+        px0[rb][k] = -1;
+        npx[rb][k] = prow[rb][k] = 0;
+        const int4 rec = bl < NT && b < p.batch ? __ldg(pp.plan.tok + b + k * p.batch) : make_int4(0, 0, 0, 0);
         const int kv = rec.z;
         if (kv == 0) continue;
         const int blk = vhead / p.heads_block, hb = vhead % p.heads_block;
@@ -601,13 +606,13 @@ __global__ void __launch_bounds__(kProjThreads, 1)
         const long long first = join64(rec.x, rec.y) + (long long)usub * unit_cost(kv) + kUnitCost;
         const int x0 = (int)(first / pquota), x1 = (int)((first + kv - 1) / pquota);
         const int tok = rec.w;
-        prow[rb] = (tok / pp.tok_tile) * 128 + (tok % pp.tok_tile) * pp.heads_tile + hb % pp.heads_tile;
-        npx[rb] = x1 - x0 + 1;
-        if (x1 > x0) px0[rb] = x0;
+        prow[rb][k] = (tok / pp.tok_tile) * 128 + (tok % pp.tok_tile) * pp.heads_tile + hb % pp.heads_tile;
+        npx[rb][k] = x1 - x0 + 1;
+        if (x1 > x0) px0[rb][k] = x0;
       }
     } else {
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) px0[rb] = npx[rb] = prow[rb] = 0;
+      for (int i = 0; i < KP * RB; ++i) px0[i / KP][i % KP] = npx[i / KP][i % KP] = prow[i / KP][i % KP] = 0;
     }
     float acc[RB][PER];
     float mx[RB], sum[RB];
@@ -620,7 +625,7 @@ __global__ void __launch_bounds__(kProjThreads, 1)
     }
     int maxseg = 0;
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) maxseg = max(maxseg, nsg[rb] + npx[rb]);
+    for (int rb = 0; rb < RB; ++rb) maxseg = max(maxseg, nsg[rb] + npx[rb][0] + (KP == 2 ? npx[rb][KP - 1] : 0));
     if (threadIdx.x == 0) MLRA_TRACE_POINT(2, 7);
     for (int s0 = 0; s0 < maxseg; s0 += SB) {
       float lv[RB][SB];
@@ -644,13 +649,16 @@ __global__ void __launch_bounds__(kProjThreads, 1)
 #pragma unroll
               for (int e = 0; e < PER; ++e) v[rb][si][e] = __ldg(src + e);
             }
-          } else if (PREFIX && s0 + si < nsg[rb] + npx[rb]) {
-            const int x = s0 + si - nsg[rb];
+          } else if (PREFIX && s0 + si < nsg[rb] + npx[rb][0] + (KP == 2 ? npx[rb][KP - 1] : 0)) {
             const PrefixParts& pp = p.prefix;
-            const size_t whole = (size_t)b * p.h + vhead;
-            const size_t cut = (size_t)(2 * (px0[rb] + x) + (x == 0 ? 1 : 0)) * pp.rows + prow[rb];
-            lv[rb][si] = __ldg(px0[rb] < 0 ? pp.lse_dense + whole : pp.part_lse + cut);
-            const float* src = px0[rb] < 0 ? pp.o_dense + whole * DBB + f0 : pp.part_o + cut * pp.dv + f0 % pp.dv;
+            int x = s0 + si - nsg[rb];
+            const bool own = KP == 2 && x >= npx[rb][0];
+            if (own) x -= npx[rb][0];
+            const int x0 = own ? px0[rb][KP - 1] : px0[rb][0];
+            const size_t whole = (size_t)(own ? b + p.batch : b) * p.h + vhead;
+            const size_t cut = (size_t)(2 * (x0 + x) + (x == 0 ? 1 : 0)) * pp.rows + (own ? prow[rb][KP - 1] : prow[rb][0]);
+            lv[rb][si] = __ldg(x0 < 0 ? pp.lse_dense + whole : pp.part_lse + cut);
+            const float* src = x0 < 0 ? pp.o_dense + whole * DBB + f0 : pp.part_o + cut * pp.dv + f0 % pp.dv;
 #pragma unroll
             for (int e = 0; e < PER; ++e) v[rb][si][e] = __ldg(src + e);
           } else {
@@ -700,7 +708,7 @@ __global__ void __launch_bounds__(kProjThreads, 1)
       for (int e = 0; e < PER; ++e) acc[rb][e] *= inv;
       if (b < rows_out && f0 == 0 && p.lse_out)  // one lane per (virtual) head
         p.lse_out[(size_t)b * p.h + vhead] =
-            nsg[rb] + npx[rb] > 0 ? (mx[rb] + __log2f(sum[rb])) * kLn2 : -INFINITY;
+            nsg[rb] + npx[rb][0] + (KP == 2 ? npx[rb][KP - 1] : 0) > 0 ? (mx[rb] + __log2f(sum[rb])) * kLn2 : -INFINITY;
       if constexpr (LATENT_ONLY) {
         if (b < p.batch) {
           float* dst = p.latent_out + ((size_t)b * p.h + head) * DB + lane * PER;

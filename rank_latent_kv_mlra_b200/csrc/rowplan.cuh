@@ -26,7 +26,8 @@ struct RowPlan {
   TokenTile* tile;     // [max tiles]
   int* base;           // [batch + 1] first token tile of each sequence
   int4* tok;           // [tokens] begin of the token's tile on the line (two words), the tile's key
-                       // tiles (0: none, or no sequence), the token's place in it; or null
+                       // tiles (0: none, or no sequence), the token's place in it; or null. With own
+                       // rows, then the same [tokens] of those
   int4* cut;           // [2 * CTAs] the unit each CTA's stretch goes on with: first and last CTA, unit;
                        // first token, tokens (written by the attention kernel, for the merge)
 };
@@ -37,6 +38,10 @@ struct RowPlanParams {
   int tile_tokens, key_tile, units;  // tokens a token tile, keys a key tile, units a token tile
   int causal;
   int ctas;            // of the attention kernel
+  // `own` sequences (total_q, or 0) in front of those of cu: sequence b is token b alone and sees
+  // own_lens[b] cached rows
+  const int* own_lens;
+  int own, own_cap;
   RowPlan plan;
   int* status;
 };
@@ -118,44 +123,51 @@ __device__ __forceinline__ int make_row_plan(const RowPlanParams& p, PlanShared&
   __syncthreads();
   int bad = 0;  // 1: a length outside its table row; 2: cu not ascending within [0, total_q]
   int running = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += threads) {
-    const int b = b0 + threadIdx.x;
+  const int seqs = p.own + p.batch;
+  for (int b0 = 0; b0 < seqs; b0 += threads) {
+    const int b = b0 + threadIdx.x, c = b - p.own;
     int tiles = 0;
-    if (b < p.batch) {
-      const int lo = p.cu[b], hi = p.cu[b + 1], n = p.lens[b];
-      if (lo < 0 || hi < lo || hi > p.total_q || (b == 0 && lo != 0)) bad |= 2;
+    if (b < p.own) {
+      const int n = p.own_lens[b];
+      if (n < 0 || n > p.own_cap) bad |= 1;
+      tiles = 1;
+    } else if (b < seqs) {
+      const int lo = p.cu[c], hi = p.cu[c + 1], n = p.lens[c];
+      if (lo < 0 || hi < lo || hi > p.total_q || (c == 0 && lo != 0)) bad |= 2;
       else tiles = (hi - lo + p.tile_tokens - 1) / p.tile_tokens;
       if (n < 0 || n > p.cap_len) bad |= 1;
     }
     int all;
     const int first = running + block_exclusive_scan<int>(tiles, scratch_i, &all);
-    if (b < p.batch) base[b] = first;
+    if (b < seqs) base[b] = first;
     running += all;
   }
   if (bad) atomicOr(&flags[0], bad);
   if (p.plan.tok != nullptr)  // tokens of no sequence
-    for (int i = threadIdx.x; i < p.total_q; i += threads) p.plan.tok[i] = make_int4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < p.total_q + p.own; i += threads) p.plan.tok[i] = make_int4(0, 0, 0, 0);
   __syncthreads();
-  // packed offsets that do not ascend leave no work at all
-  const int tiles = (flags[0] & 2) ? 0 : running;
-  if (threadIdx.x == 0) base[p.batch] = running;
+  // packed offsets that do not ascend leave no work at all (but the own rows)
+  const int tiles = (flags[0] & 2) ? p.own : running;
+  if (threadIdx.x == 0) base[seqs] = running;
   __syncthreads();
-  for (int b = threadIdx.x; b <= p.batch; b += threads) p.plan.base[b] = base[b];
+  for (int b = threadIdx.x; b <= seqs; b += threads) p.plan.base[b] = base[b];
   long long pos = 0;
   for (int i0 = 0; i0 < tiles; i0 += threads) {
     const int i = i0 + threadIdx.x;
     long long cost = 0;
     TokenTile t = {0, 0, 0, 0};
     if (i < tiles) {
-      int lo = 0, hi = p.batch;  // last b with base[b] <= i
+      int lo = 0, hi = seqs;  // last b with base[b] <= i
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (base[mid] <= i) lo = mid;
         else hi = mid;
       }
-      const int c0 = p.cu[lo], n_q = p.cu[lo + 1] - c0;
-      int len = p.lens[lo];
-      len = len < 0 ? 0 : len > p.cap_len ? p.cap_len : len;
+      const bool own = lo < p.own;
+      const int c0 = own ? lo : p.cu[lo - p.own], n_q = own ? 1 : p.cu[lo - p.own + 1] - c0;
+      const int cap = own ? p.own_cap : p.cap_len;
+      int len = own ? p.own_lens[lo] : p.lens[lo - p.own];
+      len = len < 0 ? 0 : len > cap ? cap : len;
       const int first = (i - base[lo]) * p.tile_tokens;
       t.b = lo;
       t.tok0 = c0 + first;
@@ -172,7 +184,7 @@ __device__ __forceinline__ int make_row_plan(const RowPlanParams& p, PlanShared&
       if (i < kPlanStarts) starts[i] = at;
       if (p.plan.tok != nullptr)
         for (int j = 0; j < t.ntok; ++j)
-          p.plan.tok[t.tok0 + j] = make_int4((int)at, (int)(at >> 32), key_tiles(t, p.causal, p.key_tile), j);
+          p.plan.tok[(t.b < p.own ? p.total_q : 0) + t.tok0 + j] = make_int4((int)at, (int)(at >> 32), key_tiles(t, p.causal, p.key_tile), j);
     }
     pos += all;
   }
@@ -181,7 +193,7 @@ __device__ __forceinline__ int make_row_plan(const RowPlanParams& p, PlanShared&
     p.plan.hdr[3] = flags[1];
     p.plan.start[tiles] = pos;
     p.plan.hdr[0] = tiles;
-    p.plan.hdr[1] = (flags[0] & 2) ? 0 : p.cu[p.batch];
+    p.plan.hdr[1] = p.own > 0 ? p.total_q : (flags[0] & 2) ? 0 : p.cu[p.batch];
     p.plan.hdr[2] = flags[0];
     const long long quota = stretch_of(pos, 0, p.ctas).quota;
     p.plan.hdr[4] = (int)quota;

@@ -171,6 +171,10 @@ struct RowParams {
   RowPlan plan;
   const int* page_table;   // null: page i of sequence b is b * pt_stride + i
   int pt_stride, num_pages;
+  // the first `own` sequences of the plan have pages of another table, and their results come behind
+  // the others' (o_f32, lse: [own] tokens more)
+  const int* own_table;
+  int own_stride, own;
   int causal;
   int nsub;                // (latent block, head chunk) pairs
   int chunks;              // head chunks of a block
@@ -417,14 +421,16 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         const int sub = u.sub / Sh::HALVES;
         const int blk = sub / p.chunks;
         const int pages = (tile_limit(u.t, p.causal) + kPage - 1) / kPage;
-        const size_t row = (size_t)u.t.b * p.pt_stride;
+        const bool own = u.t.b < p.own;
+        const size_t row = own ? (size_t)u.t.b * p.own_stride : (size_t)(u.t.b - p.own) * p.pt_stride;
+        const int* table = own ? p.own_table : p.page_table;
         constexpr int PPT = KT / kPage;  // pages a key tile
         int wb = u.begin * PPT;
         // page ids come through a window of two registers a lane, the next 32 read ahead
         auto ids = [&](int base) {
           const int pg = base + lane;
           if (pg >= pages) return 0;
-          return p.page_table != nullptr ? __ldg(p.page_table + row + pg) : (int)row + pg;
+          return table != nullptr ? __ldg(table + row + pg) : (int)row + pg;
         };
         int w0 = ids(wb), w1 = ids(wb + 32);
         for (int t = u.begin; t < u.end && ok; ++t, ++kt) {
@@ -826,7 +832,8 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       const int slot = 2 * blockIdx.x + (u.begin == 0 ? 1 : 0);
       const float inv = l > 0.f ? p.o_scale / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
       const float lse2 = l == 0.f ? -INFINITY : m * sc_mul + __log2f(l);
-      const size_t at = (size_t)(u.t.tok0 + tok) * p.vh + head0 + hr;
+      const int tok_out = u.t.tok0 + (u.t.b < p.own ? p.own : 0);
+      const size_t at = (size_t)(tok_out + tok) * p.vh + head0 + hr;
       const size_t pat = (size_t)slot * Sh::ROWS + q * 128 + row;
       if (mine) {
         if (!whole)
@@ -834,7 +841,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         else if (half == 0 && p.lse != nullptr)
           p.lse[at] = lse2 * p.lse_mul;
       }
-      __nv_bfloat16* const out = p.o_bf16 + ((size_t)u.t.tok0 * p.vh + head0) * Sh::DB + half * DV;
+      __nv_bfloat16* const out = p.o_bf16 + ((size_t)tok_out * p.vh + head0) * Sh::DB + half * DV;
 #pragma unroll 1
       for (int c = 0; c < DV; c += 32) {
         float o[32];
@@ -867,7 +874,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               if (tok4[r] >= u.t.ntok) continue;
-              float* dst = whole ? p.o_f32 + ((size_t)u.t.tok0 * p.vh + head0) * Sh::DB + half * DV + off4[r] -
+              float* dst = whole ? p.o_f32 + ((size_t)tok_out * p.vh + head0) * Sh::DB + half * DV + off4[r] -
                                        (lane & 3) * 8 + x
                                  : p.part_o + (pat - (lane & 3) + r) * DV + x;
               *reinterpret_cast<uint4*>(dst) = v4[r];

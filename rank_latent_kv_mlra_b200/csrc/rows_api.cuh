@@ -72,7 +72,8 @@ cudaError_t prep_rows(Variant v) {
 template <int DB, int DH, int SUMK, int NT>
 cudaError_t prep_prefix_nt() {
   using S = ProjShape<DB, DH, NT>;
-  return prep_kernel(mlra_uproj_kernel<S, false, SUMK, true>, S::SMEM4);
+  const cudaError_t e = prep_kernel(mlra_uproj_kernel<S, false, SUMK, 1>, S::SMEM4);
+  return e == cudaSuccess ? prep_kernel(mlra_uproj_kernel<S, false, SUMK, 2>, S::SMEM4) : e;
 }
 template <int DB, int DH, int SUMK>
 cudaError_t prep_prefix_proj() {
@@ -96,21 +97,22 @@ cudaError_t prep_prefix(Variant v, bool summed) {
 }
 
 template <int DB, int DH, int SUMK, int NT>
-cudaError_t launch_uproj_prefix(const mlra_ctx* h, const ProjParams& pp, int batch, cudaStream_t s) {
+cudaError_t launch_uproj_prefix(const mlra_ctx* h, const ProjParams& pp, int batch, bool own, cudaStream_t s) {
   using S = ProjShape<DB, DH, NT>;
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t c =
       launch_cfg(dim3(h->cfg.h, (batch + NT - 1) / NT), dim3(kProjThreads), S::SMEM4, s, true, &attr);
-  return cudaLaunchKernelEx(&c, mlra_uproj_kernel<S, false, SUMK, true>, h->map_wuv, pp);
+  return own ? cudaLaunchKernelEx(&c, mlra_uproj_kernel<S, false, SUMK, 2>, h->map_wuv, pp)
+             : cudaLaunchKernelEx(&c, mlra_uproj_kernel<S, false, SUMK, 1>, h->map_wuv, pp);
 }
 template <int DB, int DH, int SUMK>
-cudaError_t dispatch_uproj_prefix(const mlra_ctx* h, const ProjParams& pp, int batch, cudaStream_t s) {
+cudaError_t dispatch_uproj_prefix(const mlra_ctx* h, const ProjParams& pp, int batch, bool own, cudaStream_t s) {
   switch (nt_for(batch, max_nt<DB>())) {
-    case 16: return launch_uproj_prefix<DB, DH, SUMK, 16>(h, pp, batch, s);
-    case 32: return launch_uproj_prefix<DB, DH, SUMK, 32>(h, pp, batch, s);
-    case 64: return launch_uproj_prefix<DB, DH, SUMK, 64>(h, pp, batch, s);
+    case 16: return launch_uproj_prefix<DB, DH, SUMK, 16>(h, pp, batch, own, s);
+    case 32: return launch_uproj_prefix<DB, DH, SUMK, 32>(h, pp, batch, own, s);
+    case 64: return launch_uproj_prefix<DB, DH, SUMK, 64>(h, pp, batch, own, s);
     default:
-      if constexpr (max_nt<DB>() >= 128) return launch_uproj_prefix<DB, DH, SUMK, 128>(h, pp, batch, s);
+      if constexpr (max_nt<DB>() >= 128) return launch_uproj_prefix<DB, DH, SUMK, 128>(h, pp, batch, own, s);
       return cudaErrorInvalidValue;
   }
 }
@@ -145,7 +147,7 @@ RowsWorkspace carve_rows(const mlra_ctx* h, Carver& c, size_t tokens, size_t seq
   w.plan.tile = c.take<TokenTile>(tiles);
   w.plan.base = c.take<int>(seqs + 1);
   w.plan.cut = c.take<int4>((size_t)2 * h->num_sms);
-  w.plan.tok = per_token ? c.take<int4>(tokens) : nullptr;
+  w.plan.tok = per_token ? c.take<int4>(2 * tokens) : nullptr;  // (a second record: own rows)
   w.part_lse = c.take<float>((size_t)2 * h->num_sms * Sh::ROWS);
   w.part_o = c.take<float>((size_t)2 * h->num_sms * Sh::ROWS * Sh::DV);
   return w;
@@ -231,8 +233,8 @@ size_t prefill_bytes(const mlra_ctx* h, int total_q, int batch, int pt_stride) {
 
 struct PrefixWorkspace {
   Workspace dec;       // of the decode step over the sequences' own rows (at the workspace's start)
-  float* o;            // [batch][vh][d_b]
-  float* lse;          // [batch][vh]
+  float* o;            // [2 * batch][vh][d_b]: of the prefixes, of the own rows
+  float* lse;          // [2 * batch][vh]
   RowsWorkspace rows;
   size_t bytes;
 };
@@ -240,10 +242,10 @@ PrefixWorkspace carve_prefix(const mlra_ctx* h, int batch, int groups, void* bas
   PrefixWorkspace w;
   w.dec = carve(h, batch, base);
   Carver c = {static_cast<char*>(base), w.dec.bytes};
-  w.o = c.take<float>((size_t)batch * h->vh * h->d_b);
-  w.lse = c.take<float>((size_t)batch * h->vh);
+  w.o = c.take<float>((size_t)2 * batch * h->vh * h->d_b);
+  w.lse = c.take<float>((size_t)2 * batch * h->vh);
   w.rows = with_rows(h->var, [&](auto sh) {
-    return carve_rows<decltype(sh)>(h, c, batch, groups, heads_tile_of(h), true);
+    return carve_rows<decltype(sh)>(h, c, batch, (size_t)groups + batch, heads_tile_of(h), true);
   });
   w.bytes = c.off;
   return w;
@@ -277,6 +279,9 @@ struct RowsCall {
   const __nv_bfloat16* kv;   // per-head form: keys and values, RoPE columns
   const __nv_bfloat16* kr;
   bool causal;
+  const int* own_lens;       // own rows of every token (see RowPlanParams), or null
+  const int* own_table;
+  int own_stride;
   RowParams rp;              // results, status (the rest is filled in here)
 };
 
@@ -289,6 +294,9 @@ RowPlanParams plan_params(const mlra_ctx* h, const RowsCall& c, int* status) {
   p.total_q = c.tokens;
   p.cap_len = c.pt_stride * kPage;
   p.causal = c.causal;
+  p.own_lens = c.own_lens;
+  p.own = c.own_lens != nullptr ? c.tokens : 0;
+  p.own_cap = c.own_stride * kPage;
   p.ctas = h->num_sms;
   p.plan = c.rp.plan;
   p.status = status;
@@ -311,6 +319,9 @@ cudaError_t launch_rows(const mlra_ctx* h, const RowsCall& c, cudaStream_t s) {
   p.page_table = c.page_table;
   p.pt_stride = c.pt_stride;
   p.num_pages = c.num_pages;
+  p.own = c.own_lens != nullptr ? c.tokens : 0;
+  p.own_table = c.own_table;
+  p.own_stride = c.own_stride;
   p.causal = c.causal;
   p.nsub = Sh::SPLIT ? h->cfg.h : h->nsub;
   p.chunks = Sh::SPLIT ? 1 : h->chunks;
@@ -513,15 +524,15 @@ PrefixParts prefix_parts(const mlra_ctx* h, const RowsWorkspace& w, const float*
   });
   return pre;
 }
-cudaError_t dispatch_combine_prefix(const mlra_ctx* h, const ProjParams& pp, int batch, cudaStream_t s) {
+cudaError_t dispatch_combine_prefix(const mlra_ctx* h, const ProjParams& pp, int batch, bool own, cudaStream_t s) {
   switch (h->var) {
     case kTiny:
-      return h->summed ? dispatch_uproj_prefix<128, 32, 4>(h, pp, batch, s) : dispatch_uproj_prefix<32, 32, 1>(h, pp, batch, s);
-    case kMlra4Sum: return dispatch_uproj_prefix<512, 128, 4>(h, pp, batch, s);
-    case kMlra2: return dispatch_uproj_prefix<256, 128, 1>(h, pp, batch, s);
-    case kMlra2Sum: return dispatch_uproj_prefix<512, 128, 2>(h, pp, batch, s);
-    case kMla: return dispatch_uproj_prefix<512, 128, 1>(h, pp, batch, s);
-    default: return dispatch_uproj_prefix<128, 128, 1>(h, pp, batch, s);
+      return h->summed ? dispatch_uproj_prefix<128, 32, 4>(h, pp, batch, own, s) : dispatch_uproj_prefix<32, 32, 1>(h, pp, batch, own, s);
+    case kMlra4Sum: return dispatch_uproj_prefix<512, 128, 4>(h, pp, batch, own, s);
+    case kMlra2: return dispatch_uproj_prefix<256, 128, 1>(h, pp, batch, own, s);
+    case kMlra2Sum: return dispatch_uproj_prefix<512, 128, 2>(h, pp, batch, own, s);
+    case kMla: return dispatch_uproj_prefix<512, 128, 1>(h, pp, batch, own, s);
+    default: return dispatch_uproj_prefix<128, 128, 1>(h, pp, batch, own, s);
   }
 }
 
@@ -658,7 +669,7 @@ int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t*
       return r == cudaSuccess && !few ? launch_merge<Sh>(h, c, s) : r;
     });
   if (few) {
-    if (e == cudaSuccess) e = dispatch_combine_prefix(h, pp, total_q, s);
+    if (e == cudaSuccess) e = dispatch_combine_prefix(h, pp, total_q, false, s);
   } else if (e == cudaSuccess) {
     UpParams up = {};
     up.used = w.rows.plan.hdr + 1;
@@ -679,6 +690,24 @@ int run_prefill(mlra_handle h, const void* q, mlra_dtype q_dtype, const int32_t*
     }
   }
   return e == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
+}
+
+// Whether the attention kernel of a shared-prefix step takes the sequences' own rows too, each a
+// sequence of one token, in place of a decode kernel before it. That saves a link of the chain and
+// shares the GPU better, but a 128-row tile then holds one token's heads, and every unit of them costs
+// a query load and an epilogue: for few sequences with few own rows (their number is known on the device
+// only; the host goes by the table's capacity). Measured behind a prefix of 4096 rows, 128 heads, against
+// the decode kernel, by sequences and own rows up to: d_b = 128: 35 and 47 us at 4 and 64, 50 and 57 at 32
+// and 512, 67 and 63 at 32 and 2048, 75 and 76 at 64 and 512, 127 and 107 at 128 and 192; d_b = 256: 62 and
+// 77 at 32 and 512, 99 and 105 at 64 and 512, 213 and 141 at 128 and 64; d_b = 512: 95 and 108 at 16 and
+// 256, 294 and 286 at 64 and 512.
+bool own_in_rows(const mlra_ctx* h, int batch, int groups, int pt_stride) {
+  if (batch > 64 || groups + batch > kMaxSeqs) return false;
+  return with_rows(h->var, [&](auto sh) {
+    using Sh = decltype(sh);
+    const long long tiles = ((long long)pt_stride * kPage + Sh::KT - 1) / Sh::KT;
+    return (long long)batch * h->nsub * Sh::HALVES * (tiles + 1) <= 12LL * h->num_sms;
+  });
 }
 
 int run_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const void* pool, int num_pages,
@@ -711,11 +740,17 @@ int run_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const vo
   pp.out = out;
   pp.out_f32 = out_dtype == MLRA_F32;
   pp.lse_out = lse;
-  pp.seq_lens = seq_lens;
+  const bool own = own_in_rows(h, batch, groups, pt_stride);
+  pp.seq_lens = own ? nullptr : seq_lens;
   pp.pt_stride = pt_stride;
   pp.groups = h->groups;
 
   RowsCall c = {};
+  if (own) {
+    c.own_lens = seq_lens;
+    c.own_table = page_table;
+    c.own_stride = pt_stride;
+  }
   c.q_pack = w.dec.q_pack;
   c.tokens = batch;
   c.seqs = groups;
@@ -773,7 +808,7 @@ int run_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const vo
   pp.rows = with_rows(h->var, [&](auto sh) { return plan_params<decltype(sh)>(h, c, w.dec.status); });
   g_use_pdl = true;
   cudaError_t e = dispatch_absorb_rows(h, pp, batch, s);
-  if (e == cudaSuccess) switch (h->var) {
+  if (e == cudaSuccess && !own) switch (h->var) {
       case kTiny: e = launch_decode<DecTiny>(h, mc, mr, mqc, mqr, dp, s); break;
       case kMlra4: e = launch_decode<DecMlra4>(h, mc, mr, mqc, mqr, dp, s); break;
       case kMlra4Sum: e = launch_decode<DecMlra4Sum>(h, mc, mr, mqc, mqr, dp, s); break;
@@ -781,7 +816,7 @@ int run_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const vo
       default: e = launch_decode<DecMlra2>(h, mc, mr, mqc, mqr, dp, s); break;
     }
   if (e == cudaSuccess) e = with_rows(h->var, [&](auto sh) { return launch_rows<decltype(sh)>(h, c, s); });
-  if (e == cudaSuccess) e = dispatch_combine_prefix(h, pp, batch, s);
+  if (e == cudaSuccess) e = dispatch_combine_prefix(h, pp, batch, own, s);
   return e == cudaSuccess ? MLRA_OK : MLRA_ERR_CUDA;
 }
 

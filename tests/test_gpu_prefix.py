@@ -269,3 +269,68 @@ def test_tables_wider_than_lengths_can_be_are_refused():
         1, None)
     assert call(2 ** 25, 1) == -1 and call(1, 2 ** 25) == -1
     assert call(1, 1) == -6  # (these sizes alone: the workspace is too small)
+
+
+def widen(inp):
+    """The same step with page tables wide enough that a decode kernel takes the own rows (the library
+    goes by the table's capacity when it chooses; narrow tables leave them to the prefix's kernel)."""
+    t = inp["suf_table"]
+    return dict(inp, suf_table=torch.nn.functional.pad(t, (0, 4000 - t.shape[1]), value=-1).contiguous())
+
+
+@pytest.mark.parametrize("name", ["no_prefix", "groups", "some_without_group", "mlra2", "mla", "rank4", "tiny", "heads3",
+                                  "rank_heads", "sum4", "sum2", "tinysum"])
+def test_wide_tables_match_the_definition(name):
+    w, offsets, pre, suf = CASES[name]
+    w, inp = make(w, offsets, pre, suf, seed=len(name))
+    check(w, inp, *run(handle(w, inp), w, widen(inp)), name)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_bad_own_rows_of_both_forms(wide):
+    """Lengths, pages and offsets that are refused, a NaN that stays with its sequence, a fp32 query."""
+    w, inp = make(MLRA4, [0, 2, 5], [600, 200], [10, 0, 64, 100, 3], seed=12, q_dtype=torch.float32)
+    inp = widen(inp) if wide else inp
+    hdl = handle(w, inp)
+    check(w, inp, *run(hdl, w, inp), "fp32 query")
+    good = run(hdl, w, inp)[0]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    assert run(hdl, w, dict(inp, suf_lens=i32([10, 0, 64, 100, 10 ** 6])))[2] == -7
+    table = inp["suf_table"].clone()
+    table[3, 1] = inp["pool"].shape[0]
+    out, _, status = run(hdl, w, dict(inp, suf_table=table))
+    assert status == -4 and torch.equal(out[[0, 1, 2, 4]], good[[0, 1, 2, 4]])
+    alone = run(hdl, w, dict(inp, pre_lens=i32([0, 0])))[0]
+    out, _, status = run(hdl, w, dict(inp, offsets=i32([0, 6, 5])))
+    assert status == -7 and torch.equal(out, alone)
+    pool = inp["pool"].clone()
+    pool[int(inp["suf_table"][3, 1]), 20] = float("nan")
+    out = run(hdl, w, dict(inp, pool=pool))[0]
+    assert torch.equal(out[[0, 1, 2, 4]], good[[0, 1, 2, 4]]) and out[3].isnan().all()
+
+
+def test_rows_behind_the_groups_and_lengths_that_end_on_tiles():
+    """Own lengths around page and tile ends, every sequence of a batch at the rule's largest, and a
+    replayed graph that moves rows from one part to the other."""
+    suf = [0, 1, 63, 64, 65, 127, 128, 129, 191, 192, 193, 255, 256, 257, 319, 320] * 4
+    w, inp = make(RANK4, [0, 31, 40], [257, 128], suf, seed=13)
+    hdl = handle(w, inp)
+    check(w, inp, *run(hdl, w, inp), "64 sequences")
+    lens, offsets = inp["suf_lens"].clone(), inp["offsets"].clone()
+    out = torch.empty(64, w.h, w.d_h, device="cuda")
+    args = (inp["q"], inp["pool"], inp["pre_table"], inp["pre_lens"], inp["offsets"], inp["suf_table"],
+            inp["suf_lens"], out)
+    ws = M.mlra_decode_prefix(hdl, *args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.mlra_decode_prefix(hdl, *args, workspace=ws)
+    for new_lens, new_offsets in ((torch.zeros_like(lens), offsets), (lens, torch.zeros_like(offsets)), (lens, offsets)):
+        inp["suf_lens"].copy_(new_lens)
+        inp["offsets"].copy_(new_offsets)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        ref, _, status = run(hdl, w, inp)
+        assert status == 0 and torch.equal(got, ref)
+    check(w, inp, *run(hdl, w, inp), "after the replays")
