@@ -453,3 +453,32 @@ def test_a_replayed_graph_does_not_keep_an_earlier_status(form):
     assert replay() == -4
     inp["page_table"][0, 0] = page
     assert replay() == 0 and torch.equal(out, good)
+
+
+@BOTH
+def test_offsets_past_32_bits(form):
+    """More than 2^32 query and packed-query bytes and 2^31 result elements, a pool of more than 2^32
+    bytes: the last sequences, whose pages lie at the pool's end, against a call of their own."""
+    n, tail = 2200, 3
+    w, inp = make(MLRA4, [64] * tail, [0] * tail, seed=16, form="heads")
+    hdl = handle(w, inp)
+    ref, ref_lse, status = run(hdl, w, inp)
+    check(w, inp, ref, ref_lse, status, "alone")
+    small = inp["pool"]
+    pages = 60000
+    pool = torch.zeros(pages, *small.shape[1:], dtype=small.dtype, device="cuda")
+    pool[-small.shape[0]:] = small
+    table = torch.zeros(n, 1 if form == "heads" else 5, dtype=torch.int32, device="cuda")
+    table[-tail:, 0] = inp["page_table"][:, 0] + (pages - small.shape[0])
+    lens = torch.full((n,), 64, dtype=torch.int32, device="cuda")
+    cu = torch.arange(0, 64 * n + 1, 64, dtype=torch.int32, device="cuda")
+    q = torch.zeros(64 * n, w.h, w.d_h + w.d_r, dtype=torch.bfloat16, device="cuda")
+    q[-64 * tail:] = inp["q"]
+    out = torch.full((64 * n, w.h, w.d_h), float("nan"), dtype=torch.float32, device="cuda")
+    lse = torch.full((64 * n, w.h), float("nan"), device="cuda")
+    assert q.nbytes > 2 ** 32 and out.numel() > 2 ** 31 and pool.nbytes > 2 ** 32
+    ws = M.mlra_prefill(hdl, q, cu, pool, table, lens, out, lse)
+    torch.cuda.synchronize()
+    assert M.mlra_get_status(ws) == 0
+    check(w, inp, out[-64 * tail:], lse[-64 * tail:], 0, "behind others")
+    assert not out[:64].any() and not out[64 * 1000:64 * 1001].any()
