@@ -362,11 +362,12 @@ def _call(name, dev, stream, *args):
 
 
 def _new_workspace(size: int, dev, stream):
-    """A workspace of `size` bytes that outlives the work on `stream`."""
-    workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        workspace.record_stream(stream)
-    return workspace
+    """A workspace of `size` bytes from the pool of the stream that the call runs on: a block of the
+    current stream's may still be in use by work queued there, which `stream` does not wait for."""
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=dev)
 
 
 def _addr(t):

@@ -1,0 +1,96 @@
+"""Calls on a stream that is not the current one, without a workspace of the caller's: what they take for
+themselves must not be memory that work queued on the current stream still uses. A block that such work
+is about to write and read is freed, and a call on another stream made at once: it must not be handed
+that block, the queued work's result must be whole, and the call's own result the usual one."""
+import pytest
+import torch
+
+import rank_latent_kv_mlra_b200 as M
+import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+TINY = W.scaled(W.WORKLOADS["mlra4_h8_b1_n256_f32"], batch=3, seq_len=None, len_range=(100, 200), seed=70)
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    M.load_library()
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def behind_queued_work(size, call):
+    """call(stream) -> its workspace, made while the current stream is busy and the block of `size`
+    bytes that its queued work uses has been freed."""
+    busy = torch.ones(4096, 4096, device="cuda")
+    prod, kept = torch.empty_like(busy), torch.zeros(size, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.Stream()
+    block = torch.empty(size, dtype=torch.uint8, device="cuda")
+    lo = block.data_ptr()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        torch.mm(busy, busy, out=prod)
+    block.fill_(7)
+    kept.copy_(block)
+    del block
+    ws = call(stream)
+    torch.cuda.synchronize()
+    assert bool((kept == 7).all())
+    assert ws.data_ptr() + ws.numel() <= lo or ws.data_ptr() >= lo + size
+    assert M.mlra_get_status(ws) == 0
+
+
+def _tiny():
+    inp = W.make_workload(TINY, device="cuda")
+    hdl = M.mlra_create(TINY.h, TINY.d_h, TINY.d_c, TINY.d_r, TINY.k, inp["w_uk"], inp["w_uv"])
+    return inp, hdl
+
+
+def test_prefill():
+    inp, hdl = _tiny()
+    table = inp["page_table"]
+    q = torch.randn(70, TINY.h, TINY.d_h + TINY.d_r, device="cuda").bfloat16()
+    out = torch.empty(70, TINY.h, TINY.d_h, device="cuda")
+    args = (hdl, q, i32([0, 30, 31, 70]), inp["pool"], table, inp["seq_lens"], out)
+    M.mlra_prefill(*args)
+    want = out.clone()
+    out.zero_()
+    behind_queued_work(M.mlra_prefill_workspace_size(hdl, 70, 3, table.shape[1]),
+                       lambda s: M.mlra_prefill(*args, stream=s))
+    assert torch.equal(out, want)
+
+
+def test_decode_prefix():
+    inp, hdl = _tiny()
+    table, lens = inp["page_table"], inp["seq_lens"]
+    q = torch.randn(2, TINY.h, TINY.d_h + TINY.d_r, device="cuda").bfloat16()
+    out = torch.empty(2, TINY.h, TINY.d_h, device="cuda")
+    args = (hdl, q, inp["pool"], table[:1].contiguous(), lens[:1].contiguous(), i32([0, 2]), table[1:].contiguous(),
+            lens[1:].contiguous(), out)
+    M.mlra_decode_prefix(*args)
+    want = out.clone()
+    out.zero_()
+    behind_queued_work(M.mlra_decode_prefix_workspace_size(hdl, 2, 1), lambda s: M.mlra_decode_prefix(*args, stream=s))
+    assert torch.equal(out, want)
+
+
+def test_page_operators():
+    inp, hdl = _tiny()
+    P = inp["pool"].shape[0]
+    refs, table, lens = i32([0] * P), i32([[-1] * 2] * 3), i32([0] * 3)
+    state = (refs, table, lens)
+    size = M.mlra_pages_workspace_size(hdl, P, 3)
+    row, other, new = i32([1]), i32([2]), i32([70])
+    behind_queued_work(size, lambda s: M.mlra_reserve_pages(hdl, *state, row, new, stream=s))
+    assert table.tolist() == [[-1, -1], [0, 1], [-1, -1]]
+    behind_queued_work(size, lambda s: M.mlra_fork_pages(hdl, inp["pool"], *state, row, other, stream=s))
+    assert table.tolist() == [[-1, -1], [0, 1], [0, 2]] and lens.tolist() == [0, 70, 70]
+    behind_queued_work(size, lambda s: M.mlra_free_pages(hdl, *state, row, stream=s))
+    assert lens.tolist() == [0, 0, 70] and refs.tolist()[:3] == [1, 0, 1]
+    behind_queued_work(size, lambda s: M.mlra_compact_pages(hdl, inp["pool"], *state, stream=s))
+    assert table[2].tolist() == [0, 1] and refs.tolist()[:3] == [1, 1, 0]
