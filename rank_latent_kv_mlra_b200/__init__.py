@@ -180,8 +180,18 @@ def mlra_workspace_size(handle: Handle, batch: int) -> int:
 
 
 def alloc_workspace(handle: Handle, batch: int, device=None) -> torch.Tensor:
-    """Workspace for `batch` sequences (a uint8 CUDA tensor; torch allocations are 256-aligned)."""
+    """Workspace for `batch` sequences (a uint8 CUDA tensor; torch allocations are 256-aligned), from
+    the current stream's pool: for calls on it, or on streams that wait for it."""
     return torch.empty(mlra_workspace_size(handle, batch), dtype=torch.uint8, device=device or "cuda")
+
+
+def _new_workspace(size: int, dev, stream):
+    """A workspace of `size` bytes from the pool of the stream that the call runs on: a block of the
+    current stream's may still be in use by work queued there, which `stream` does not wait for."""
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=dev)
 
 
 def mlra_get_info(handle: Handle) -> dict:
@@ -215,7 +225,7 @@ def mlra_decode(handle: Handle, q, pool, page_table, seq_lens, out, lse=None, wo
                 stream=None):
     """One decode step; `out` [batch][h][d_h] (fp32 or bf16), `lse` fp32 [batch][h] or None."""
     if workspace is None:
-        workspace = alloc_workspace(handle, q.shape[0], q.device)
+        workspace = _new_workspace(mlra_workspace_size(handle, q.shape[0]), q.device, stream)
     B = _decode_common(handle, q, pool, page_table, seq_lens, workspace)
     _require(out, "out")
     if lse is not None:
@@ -261,7 +271,7 @@ def mlra_decode_profiled(handle: Handle, q, pool, page_table, seq_lens, out, eve
                          workspace=None, stream=None):
     """mlra_decode that records four torch.cuda.Event objects around its three kernels."""
     if workspace is None:
-        workspace = alloc_workspace(handle, q.shape[0], q.device)
+        workspace = _new_workspace(mlra_workspace_size(handle, q.shape[0]), q.device, stream)
     B = _decode_common(handle, q, pool, page_table, seq_lens, workspace)
     for e in events:
         if e.cuda_event == 0:  # torch creates the CUDA event on its first record
@@ -278,7 +288,7 @@ def mlra_decode_latent(handle: Handle, q, pool, page_table, seq_lens, latent_out
                        workspace=None, stream=None):
     """Decode without the up-projection: `latent_out` fp32 [batch][h][d_c/k]."""
     if workspace is None:
-        workspace = alloc_workspace(handle, q.shape[0], q.device)
+        workspace = _new_workspace(mlra_workspace_size(handle, q.shape[0]), q.device, stream)
     B = _decode_common(handle, q, pool, page_table, seq_lens, workspace)
     _require(latent_out, "latent_out", torch.float32)
     if lse is not None:
@@ -329,8 +339,7 @@ def mlra_project_append(handle: Handle, x, w_down, positions, pool, page_table, 
     if positions.shape != (B,) or page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("positions must be [batch], page_table [batch][pt_stride]")
     if workspace is None:
-        workspace = torch.empty(mlra_project_workspace_size(handle, B, d_model), dtype=torch.uint8,
-                                device=x.device)
+        workspace = _new_workspace(mlra_project_workspace_size(handle, B, d_model), x.device, stream)
     _require(workspace, "workspace")
     _check(load_library().mlra_project_append(
         handle.ptr, _ptr(x), d_model, _ptr(w_down), float(rope_base), _ptr(positions), _ptr(pool),
@@ -359,15 +368,6 @@ def _call(name, dev, stream, *args):
             rc = fn(*args, raw)
     if rc != 0:
         raise MlraError(rc, name)
-
-
-def _new_workspace(size: int, dev, stream):
-    """A workspace of `size` bytes from the pool of the stream that the call runs on: a block of the
-    current stream's may still be in use by work queued there, which `stream` does not wait for."""
-    if stream is None:
-        return torch.empty(size, dtype=torch.uint8, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(size, dtype=torch.uint8, device=dev)
 
 
 def _addr(t):
@@ -540,13 +540,14 @@ def mlra_compact_pages(handle: Handle, pool, refs, page_table, seq_lens, used=No
 def mlra_plan(handle: Handle, seq_lens, pt_stride: int, max_segments: int = 4096, stream=None):
     """Device split plan as a list of (b, group, tile_begin, tile_end, slot) tuples."""
     _require(seq_lens, "seq_lens", torch.int32)
-    segs = torch.zeros((max_segments, 5), dtype=torch.int32, device=seq_lens.device)
-    count = torch.zeros(1, dtype=torch.int32, device=seq_lens.device)
-    _check(load_library().mlra_plan(handle.ptr, _ptr(seq_lens), seq_lens.numel(), pt_stride,
-                                    _ptr(segs), max_segments, _ptr(count), _stream(stream)),
-           "mlra_plan")
-    n = int(count.item())
-    return [tuple(r) for r in segs[:min(n, max_segments)].tolist()], n
+    with torch.cuda.stream(stream):  # cleared, filled and read in that stream's order (None: the current one)
+        segs = torch.zeros((max_segments, 5), dtype=torch.int32, device=seq_lens.device)
+        count = torch.zeros(1, dtype=torch.int32, device=seq_lens.device)
+        _check(load_library().mlra_plan(handle.ptr, _ptr(seq_lens), seq_lens.numel(), pt_stride,
+                                        _ptr(segs), max_segments, _ptr(count), _stream(stream)),
+               "mlra_plan")
+        n = int(count.item())
+        return [tuple(r) for r in segs[:min(n, max_segments)].tolist()], n
 
 
 def mlra_get_status(status_word: torch.Tensor) -> int:

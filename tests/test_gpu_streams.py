@@ -79,6 +79,46 @@ def test_decode_prefix():
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("latent", [False, True])
+def test_decode(latent):
+    inp, hdl = _tiny()
+    fn = M.mlra_decode_latent if latent else M.mlra_decode
+    out = torch.empty(3, TINY.h, TINY.d_c // TINY.k if latent else TINY.d_h, device="cuda")
+    args = (hdl, inp["q"], inp["pool"], inp["page_table"], inp["seq_lens"], out)
+    fn(*args)
+    want = out.clone()
+    out.zero_()
+    behind_queued_work(M.mlra_workspace_size(hdl, 3), lambda s: fn(*args, stream=s))
+    assert torch.equal(out, want)
+
+
+def test_project_append():
+    inp, hdl = _tiny()
+    pr = W.make_producer_inputs(TINY, inp, d_model=256)
+    args = (hdl, pr["x"], pr["w_down"], pr["positions"], inp["pool"], inp["page_table"])
+    M.mlra_project_append(*args)
+    want = inp["pool"].clone()
+    inp["pool"].zero_()
+    behind_queued_work(M.mlra_project_workspace_size(hdl, 3, 256), lambda s: M.mlra_project_append(*args, stream=s))
+    for b, pos in enumerate(pr["positions"].tolist()):
+        page = int(inp["page_table"][b, pos // 64])
+        assert torch.equal(inp["pool"][page, pos % 64], want[page, pos % 64])
+
+
+def test_plan():
+    """The plan's rows are cleared, filled and read in the order of the call's stream."""
+    inp, hdl = _tiny()
+    stride = inp["page_table"].shape[1]
+    want = M.mlra_plan(hdl, inp["seq_lens"], stride)
+    assert want[1] > 0
+    busy = torch.ones(4096, 4096, device="cuda")
+    prod, stream = torch.empty_like(busy), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        torch.mm(busy, busy, out=prod)
+    assert M.mlra_plan(hdl, inp["seq_lens"], stride, stream=stream) == want
+
+
 def test_page_operators():
     inp, hdl = _tiny()
     P = inp["pool"].shape[0]

@@ -24,6 +24,10 @@ class _Stream:
     cuda_stream = 0
 
 
+class _Event:
+    cuda_event = 1
+
+
 def i32(*shape):
     return torch.zeros(*shape, dtype=torch.int32)
 
@@ -33,9 +37,14 @@ def bf16(*shape):
 
 
 Q, POOL, OUT = bf16(3, 128, 192), bf16(4, 64, 576), bf16(3, 128, 128)
+LENS = i32(3)
 CALLS = {
     "mlra_prefill": (Q, i32(2), POOL, i32(1, 4), i32(1), OUT),
     "mlra_decode_prefix": (Q, POOL, i32(1, 4), i32(1), i32(2), i32(3, 4), i32(3), OUT),
+    "mlra_decode": (Q, POOL, i32(3, 4), i32(3), OUT),
+    "mlra_decode_latent": (Q, POOL, i32(3, 4), i32(3), torch.zeros(3, 128, 128)),
+    "mlra_decode_profiled": (Q, POOL, i32(3, 4), i32(3), OUT, [_Event()] * 4),
+    "mlra_project_append": (bf16(3, 128), bf16(576, 128), i32(3), POOL, i32(3, 4)),
 }
 
 
@@ -63,11 +72,12 @@ def taken(monkeypatch):
     monkeypatch.setattr(M, "load_library", lambda: _Lib())
     monkeypatch.setattr(M, "_require", lambda *a: None)
     monkeypatch.setattr(M, "_call", lambda *a: None)
+    monkeypatch.setattr(M, "_stream", lambda stream: None)
     return where
 
 
-@pytest.mark.parametrize("name", ["mlra_prefill", "mlra_decode_prefix"])
-def test_attention_workspaces_belong_to_the_call_s_stream(taken, name):
+@pytest.mark.parametrize("name", list(CALLS))
+def test_workspaces_belong_to_the_call_s_stream(taken, name):
     getattr(M, name)(_Handle, *CALLS[name], stream=None)
     assert taken == [None]
     stream = _Stream()
@@ -81,3 +91,10 @@ def test_page_workspaces_belong_to_the_call_s_stream(taken):
     M._new_workspace(16, torch.device("cpu"), stream)
     M._new_workspace(16, torch.device("cpu"), None)
     assert taken == [stream, None]
+
+
+def test_the_plan_is_cleared_and_read_on_the_call_s_stream(taken):
+    stream, lens = _Stream(), LENS
+    M.mlra_plan(_Handle, lens, 4, stream=stream)
+    M.mlra_plan(_Handle, lens, 4)
+    assert taken == [stream, stream, None, None]
