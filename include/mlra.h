@@ -237,7 +237,9 @@ int mlra_project_append(mlra_handle h, const void* x, int d_model, const void* w
  * query token with 128 heads of 128 (packed query and latent result), plus a fixed part of some
  * 40 MB; with an E4M3 cache also the bf16 form of batch * pt_stride pages. A call whose page table
  * holds at most four times its query tokens (whole prompts) keeps every head's keys and values
- * instead, 64 KB a row of the table's capacity, so that a narrower table may need more than a wide one. */
+ * instead, 64 KB a row of the table's capacity, so that a narrower table may need more than a wide one.
+ * The size never falls as total_q grows: a workspace for total_q tokens serves every call with fewer
+ * of them at the same batch and pt_stride. */
 int mlra_prefill_workspace_size(mlra_handle h, int total_q, int batch, int pt_stride, size_t* bytes);
 
 /* Causal attention of the query tokens of packed sequences (whole prompts, or the next tokens of

@@ -177,7 +177,8 @@ bool per_head_sizes(const mlra_ctx* h, int total_q, int batch, int pt_stride) {
 // kernel, in place of the merge and the up-projection of many tokens. Measured (four sequences of 128
 // heads, contexts of 2000), both ways: d_b = 128: 28.7 and 29.0 us at 16 tokens, 32.2 and 34.9 at 32,
 // 43.1 and 43.6 at 64, 59.1 and 55.4 at 128; d_b = 256: 38.6 and 38.1 at 16, 55.3 and 51.2 at 64.
-bool few_tokens(const mlra_ctx* h, int total_q) { return total_q <= 32 && h->d_b <= 128 && !h->summed; }
+constexpr int kFewTokens = 32;
+bool few_tokens(const mlra_ctx* h, int total_q) { return total_q <= kFewTokens && h->d_b <= 128 && !h->summed; }
 
 struct PrefillWorkspace {
   int* status;
@@ -225,7 +226,11 @@ HeadWorkspace carve_head(const mlra_ctx* h, int total_q, int batch, int pt_strid
   return w;
 }
 size_t prefill_bytes(const mlra_ctx* h, int total_q, int batch, int pt_stride) {
-  const size_t a = carve_prefill(h, total_q, batch, pt_stride, nullptr).bytes;
+  size_t a = carve_prefill(h, total_q, batch, pt_stride, nullptr).bytes;
+  // Few tokens keep fp32 latents and a record a token, which more tokens do without: a call's workspace
+  // holds any smaller call's as well.
+  const size_t few = carve_prefill(h, total_q < kFewTokens ? total_q : kFewTokens, batch, pt_stride, nullptr).bytes;
+  if (few > a) a = few;
   if (!per_head_sizes(h, total_q, batch, pt_stride)) return a;
   const size_t b = carve_head(h, total_q, batch, pt_stride, nullptr).bytes;
   return a > b ? a : b;  // (an fp32 query takes the absorbed form)
