@@ -19,9 +19,11 @@ DEPS = SOURCES + [os.path.join(HERE, "csrc", f) for f in os.listdir(os.path.join
 
 
 def nvcc_command(ptxas_verbose=False):
+    # --no-compress: a process's first handle loads the whole module. Measured, its creation with the
+    # 25 MB stored as they are and packed into 7: 19 and 31 ms (later handles: 2.5).
     nvcc = os.environ.get("NVCC", "nvcc")
     cmd = [nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-           "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC", "-shared", "-cudart", "static",
+           "--expt-relaxed-constexpr", "--no-compress", "-Xcompiler", "-fPIC", "-shared", "-cudart", "static",
            "-I", os.path.join(ROOT, "include"), "-o", LIB] + SOURCES
     if ptxas_verbose:
         cmd.insert(1, "-Xptxas=-v")
