@@ -836,9 +836,11 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
       const size_t at = (size_t)(tok_out + tok) * p.vh + head0 + hr;
       const size_t pat = (size_t)slot * Sh::ROWS + q * 128 + row;
       if (mine) {
+        // (column halves are cut on their own: the one that is whole writes its lse even where the other
+        // is not; where both are, they write the same bits, having formed the same scores)
         if (!whole)
           p.part_lse[pat] = lse2;
-        else if (half == 0 && p.lse != nullptr)
+        else if (p.lse != nullptr)
           p.lse[at] = lse2 * p.lse_mul;
       }
       __nv_bfloat16* const out = p.o_bf16 + ((size_t)tok_out * p.vh + head0) * Sh::DB + half * DV;

@@ -334,3 +334,26 @@ def test_rows_behind_the_groups_and_lengths_that_end_on_tiles():
         ref, _, status = run(hdl, w, inp)
         assert status == 0 and torch.equal(got, ref)
     check(w, inp, *run(hdl, w, inp), "after the replays")
+
+
+HALVES = {
+    # many short units a CTA, so that a boundary cuts one column half's unit and leaves the other's whole
+    "own_rows": (MLA, [0, 49, 63], [261, 41], [(37 * i) % 300 if i % 3 else 1 for i in range(64)]),
+    "rank_of_own_rows": (W.scaled(MLA, h=16), [0, 20], [200], [(53 * i) % 300 for i in range(60)]),
+    "prefixes": (MLA, list(range(0, 101)), [(29 * i) % 400 for i in range(100)], [i % 3 for i in range(100)]),
+    "own_rows_mlra2": (MLRA2, [0, 49, 63], [261, 41], [(37 * i) % 300 if i % 3 else 1 for i in range(64)]),
+    "own_rows_sum4": (SUM4, [0, 9], [261], [(37 * i) % 200 for i in range(40)]),
+}
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("name", list(HALVES))
+def test_units_of_which_one_half_is_cut(name, wide):
+    """In a workspace of NaN bits, so that a result that no unit of the call has written shows."""
+    w, offsets, pre, suf = HALVES[name]
+    w, inp = make(w, offsets, pre, suf, seed=21)
+    inp = widen(inp) if wide else inp
+    hdl = handle(w, inp)
+    size = M.mlra_decode_prefix_workspace_size(hdl, len(suf), len(pre))
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    check(w, inp, *run(hdl, w, inp, workspace=ws), name)
