@@ -71,3 +71,33 @@ def test_a_workspace_for_more_tokens_serves_fewer():
             assert M.mlra_get_status(got) == 0
             outs.append(out)
         assert torch.equal(*outs)
+
+
+KINDS = [("mlra4_h128_b32_n8192", [3, 20], [700, 40], 0), ("mlra4_h128_b32_n8192", [33, 90, 0, 1], [10, 900, 64, 0], 0),
+         ("mlra4_h128_b32_n8192", [700, 300], [0, 0], 0), ("mlra2_h128_b64_n4096", [5, 130], [900, 40], 30),
+         ("mla_h128_b128_ragged1k_32k", [1] * 70, [7 * i for i in range(70)], 0),
+         ("mla_h128_b128_ragged1k_32k", [300, 257], [0, 0], 0), ("mlra4fp8_h128_b32_n8192", [5, 130], [900, 40], 0),
+         ("mlra4sum_h128_b32_n8192", [5, 70], [40, 300], 0)]
+
+
+@pytest.mark.parametrize("name,n,past,spare", KINDS)
+def test_results_do_not_depend_on_what_the_workspace_held(name, n, past, spare):
+    """Prompt calls of every form in workspaces of zeros and of NaN bits: the same bits."""
+    w = W.scaled(W.WORKLOADS[name], batch=len(n), seq_len=None, len_range=(1, 1), seed=82)
+    lens = torch.tensor([a + b for a, b in zip(n, past)], dtype=torch.int32)
+    inp = W.make_workload(w, device="cuda", seq_lens=lens)
+    table = torch.nn.functional.pad(inp["page_table"], (0, spare), value=-1).contiguous()
+    hdl = handle(w, inp["w_uk"], inp["w_uv"])
+    q = torch.randn(sum(n), w.h, w.d_h + w.d_r, device="cuda").bfloat16()
+    cu = torch.tensor([sum(n[:b]) for b in range(len(n) + 1)], dtype=torch.int32, device="cuda")
+    size = M.mlra_prefill_workspace_size(hdl, sum(n), len(n), table.shape[1])
+    outs = []
+    for fill in (0, 255):
+        ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        out = torch.full((sum(n), w.h, w.d_h), float("nan"), device="cuda")
+        lse = torch.full((sum(n), w.h * (w.k if w.summed else 1)), float("nan"), device="cuda")
+        M.mlra_prefill(hdl, q, cu, inp["pool"], table, inp["seq_lens"], out, lse, workspace=ws)
+        torch.cuda.synchronize()
+        assert M.mlra_get_status(ws) == 0 and not out.isnan().any() and not lse.isnan().any()
+        outs.append((out, lse))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
