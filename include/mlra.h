@@ -233,11 +233,14 @@ int mlra_project_append(mlra_handle h, const void* x, int d_model, const void* w
                         const int32_t* positions, void* pool, int num_pages, const int32_t* page_table,
                         int pt_stride, int batch, void* workspace, size_t ws_bytes, void* stream);
 
-/* Bytes of device workspace mlra_prefill needs for a call of these sizes (host output): about 80 KB a
- * query token with 128 heads of 128 (packed query and latent result), plus a fixed part of some
- * 40 MB; with an E4M3 cache also the bf16 form of batch * pt_stride pages. A call whose page table
- * holds at most four times its query tokens (whole prompts) keeps every head's keys and values
- * instead, 64 KB a row of the table's capacity, so that a narrower table may need more than a wide one.
+/* Bytes of device workspace mlra_prefill needs for a call of these sizes (host output). A query token
+ * takes 2 * H * (2 * d_b + d_rope) bytes, d_b = d_c/k and H = h (k*h with blocks_summed), for its packed
+ * query and latent result (128 heads: 80 KB at d_b = 128, 144 at 256, 272 at 512, 320 summed over four
+ * blocks of 128; where a block has few heads its packed query counts as 16, 32 or 64 of them), plus a
+ * fixed part of 39 to 40 MB at d_b >= 128; with an E4M3 cache also the bf16 form of batch * pt_stride
+ * pages. A call whose page table holds at most four times its query tokens (whole
+ * prompts) keeps every head's keys and values instead, 512 bytes a head and row of the table's capacity
+ * (64 KB a row at 128 heads), so that a narrower table may need more than a wide one.
  * The size never falls as total_q grows: a workspace for total_q tokens serves every call with fewer
  * of them at the same batch and pt_stride. */
 int mlra_prefill_workspace_size(mlra_handle h, int total_q, int batch, int pt_stride, size_t* bytes);
@@ -252,7 +255,8 @@ int mlra_prefill_workspace_size(mlra_handle h, int total_q, int batch, int pt_st
  *              16-byte aligned. total_q <= 2^21. An fp32 query is rounded to bf16.
  *   cu_seqlens device int32 [batch + 1], ascending from 0 to at most total_q; sequence b's tokens
  *              are rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (none: n_b = 0). Rows from
- *              cu_seqlens[batch] on belong to no sequence; their out and lse stay as they were.
+ *              cu_seqlens[batch] on belong to no sequence: what q holds there has no effect, and their
+ *              out and lse stay as they were.
  *              Offsets that do not ascend leave all of out and lse as they were and report
  *              MLRA_ERR_SEQ_LEN.
  *   pool, num_pages, page_table, pt_stride: as in mlra_decode. Sequences may share pages.

@@ -358,7 +358,9 @@ def _one_device(names, *tensors):
 
 
 def _call(name, dev, stream, *args):
-    """Calls the library's `name` on `dev`, with the stream (None: the device's current one) last."""
+    """Calls the library's `name` on `dev`, with the stream (None: the device's current one) last.
+    (Torch's own lookups of the current stream and device: 0.2 us a call, where
+    torch.cuda.current_stream(dev).cuda_stream takes 2.2, and a scheduler's turn makes three calls.)"""
     fn = getattr(load_library(), name)
     raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == dev.index:
@@ -410,9 +412,9 @@ def mlra_prefill(handle: Handle, q, cu_seqlens, pool, page_table, seq_lens, out,
     """Causal attention of packed prompt tokens over their sequences' cached rows. Rows
     cu_seqlens[b] .. cu_seqlens[b+1] - 1 of `q` [total][h][d_h + d_rope] are the last tokens of
     sequence b, whose seq_lens[b] cached rows include their own; `out` [total][h][d_h] (fp32 or
-    bf16), `lse` fp32 [total][h] ([total][k*h] with summed blocks) or None. Rows of q behind
-    cu_seqlens[batch] are not read and their out and lse are left as they were. Returns the
-    workspace, whose first int32 is the call's status word."""
+    bf16), `lse` fp32 [total][h] ([total][k*h] with summed blocks) or None. What rows of q
+    behind cu_seqlens[batch] hold has no effect, and their out and lse are left as they were. Returns
+    the workspace, whose first int32 is the call's status word."""
     total = q.shape[0]
     _attention_args(handle, q, total, pool, out, lse)
     _tables(page_table, seq_lens, ("page_table", "seq_lens"))

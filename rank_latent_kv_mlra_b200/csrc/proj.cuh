@@ -44,7 +44,7 @@ struct ProjParams {
   // absorb
   const void* q;      // [B][h][d_h + d_r]
   int q_f32;          // 1: fp32 q, 0: bf16 q
-  __nv_bfloat16* q_pack;  // [B][nsub][NP][DB + DR]
+  __nv_bfloat16* q_pack;  // [B][nsub][NP][DB + DR], rounded once (half a step 2^-8) for the scores' MMAs
   float qscale;       // softmax scale * log2(e), of q^C
   float qscale_rope;  // of q^R (bf16 packed query)
   int d_r;
@@ -716,7 +716,8 @@ __global__ void __launch_bounds__(kProjThreads, 1)
           for (int e = 0; e < PER; ++e) dst[e] = acc[rb][e];
         }
       } else {
-        // lane's PER features start at byte lane*PER*2 of the row
+        // lane's PER features start at byte lane*PER*2 of the row; the merged latent is rounded to bf16
+        // here (half a step 2^-8 relative), the up-projection's operand
 #pragma unroll
         for (int e = 0; e < PER; e += 2) {
           const int f = lane * PER + e;

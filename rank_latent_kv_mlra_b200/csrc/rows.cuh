@@ -19,9 +19,10 @@
 // (1280; the scores' MMAs, both operands from shared memory at N = 128, measure 85 each) against
 // 16384 exponentials (1024 clocks of the special-function units), so two row tiles run in turn: one
 // tile's softmax works while the other's MMAs run. Measured per pair of tiles: 3200 to 3300 clocks,
-// of which the softmax of one tile takes 2800 and the MMAs of both 3060. One step over a 32768-row
-// prefix for 128 sequences of 128 heads (350 GFLOP) takes 290 us, 1.2 PFLOP/s; a 16384-token prompt
-// (11.1 TFLOP) 8.5 ms, 1.3 PFLOP/s, with the clock at 1.6 GHz of 1.965 under the 1000 W power cap.
+// of which the softmax of one tile takes 2800 and the MMAs of both 3060. This kernel alone: one step
+// over a 32768-row prefix for 128 sequences of 128 heads (350 GFLOP) takes 290 us, 1.2 PFLOP/s; a
+// 16384-token prompt (11.1 TFLOP) 8.5 ms, 1.3 PFLOP/s, with the clock at 1.6 GHz of 1.965 under the
+// 1000 W power cap (the whole call 9.4 ms, 10.2 in long runs).
 // Steps that got there, on that prompt as a whole call: one MMA warp and plan walks by every role 13.1
 // ms; a walk warp, uniform-register MMA issue and the register split 10.3; separate issuers of scores
 // and values with one score buffer in turn 9.7; masks and results in fewer instructions 9.35.
@@ -852,7 +853,7 @@ __global__ void __launch_bounds__(Sh::THREADS, 1)
         // (a row tile without a key tile in this part has no O)
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = n > 0 ? o[e] * inv : 0.f;
-        if (whole && p.o_bf16 != nullptr) {
+        if (whole && p.o_bf16 != nullptr) {  // (half a step 2^-8 relative: the up-projection's operand, or out)
           uint4 v4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -932,6 +933,7 @@ __global__ void __launch_bounds__(256) mlra_rows_merge_kernel(const MergeParams 
   grid_launch_dependents();
   const int warp = warp_id(), lane = lane_id(), nwarp = blockDim.x >> 5;
   const int slice = blockIdx.y * nwarp + warp, slices = gridDim.y * nwarp;
+  // (a latent result to bf16, half a step 2^-8 relative, for the up-projection's MMAs)
   auto put = [&](size_t at, float v) {
     if (p.o_bf16 != nullptr) p.o_bf16[at] = __float2bfloat16_rn(v);
     else p.o_f32[at] = v;
@@ -1037,6 +1039,7 @@ struct UpShape {
 // a token and head: TMA stores of staged tiles, because 64-byte pieces from registers cost more in
 // lane exchanges than the product (24,800 tokens of 128 heads: 535 us). The blocks also copy the RoPE
 // columns to rows of their own.
+// Keys and values are rounded to bf16 (half a step 2^-8 relative), the attention's operands.
 // Values are stored finite, infinities and NaN as the largest bf16 values: a masked key's P = 0 then
 // adds nothing. A token that does see a cached row with NaN or infinities gets NaN through the
 // row's keys, which keep them.
@@ -1100,7 +1103,8 @@ __global__ void __launch_bounds__(Sh::THREADS)
   const int items = tiles * p.heads * (EXPAND ? 2 : 1);  // (the host keeps this within 32 bits)
   const int per = (items + gridDim.x - 1) / gridDim.x;
   const int lo = (int)min((long long)per * blockIdx.x, (long long)items), hi = min(lo + per, items);
-  // item = head * tiles + tile, followed step by step: a division an item was most of a role's time
+  // item = head * tiles + tile, followed step by step: divisions for both of an item's numbers were most
+  // of a role's time (EXPAND's skip still divides by seq_tiles, once an item and role)
   const int h_lo = tiles > 0 ? lo / tiles : 0, tile_lo = lo - h_lo * tiles;
   auto step = [&](int& h, int& tile) {
     if (++tile == tiles) {

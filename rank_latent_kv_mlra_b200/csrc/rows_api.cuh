@@ -7,7 +7,7 @@ namespace {
 // Shapes of the row attention, one a set of block dims. MLRA-4 blocks (d_b = 128) run two row tiles in
 // turn; at d_b = 256 a row tile's O fills half the tensor memory, so one row tile alternates two
 // score buffers over 64-key tiles; at d_b = 512 two CTAs keep a half of O each and both form the
-// scores (1664 FLOPs a query, key and head in place of 1088, but nothing passes between SMs).
+// scores (3328 FLOPs a query, key and head in place of 2176, but nothing passes between SMs).
 using RowsTiny = RowShape<32, 16, 128, 32, 2, 4, 4>;
 using RowsB128 = RowShape<128, 64, 128, 128, 2, 3, 2>;
 using RowsB256 = RowShape<256, 64, 64, 256, 1, 3, 3>;
@@ -158,15 +158,19 @@ int heads_tile_of(const mlra_ctx* h) { return h->heads_block < h->np ? h->heads_
 long long seq_rows_of(int pt_stride) { return ((long long)pt_stride + 1) / 2 * kTile; }
 
 // Whether a prompt call of these sizes takes the per-head form (unless its query is fp32): form every
-// head's keys and values of the cached rows once, then attend with keys of d_h + d_rope and values
-// of d_h. Against the absorbed form it saves MMA work where d_b > d_h (640 against 1152 FLOPs a
-// query, key and head at d_b = 256, 2176 at 512) and the two projections' query-sided traffic, and
-// costs 512 bytes a cached token and head: worth it where the cached rows are few against the query
-// tokens. Their number is known on the device only; the host goes by the table's capacity.
-// Measured, one prompt of 128 heads, against the absorbed form: d_b = 128: 243 and 288 us at 2048
-// tokens, 753 and 789 at 4096, 9.46 and 9.40 ms at 16384 (24 ragged prompts up to 2047 tokens: 2.21
-// and 2.53 ms); d_b = 256: 0.78 and 1.81 ms at 4096; d_b = 512: 82 and 249 us at 512, 0.84 and 6.8 ms
-// at 4096.
+// head's keys and values of the cached rows once, then attend with keys of d_h + d_rope and values of
+// d_h: 640 FLOPs a query, key and head, against 640, 1152 and 3328 of the absorbed form at d_b = 128,
+// 256 and 512 (where it forms the scores twice), and without its two projections' query-sided traffic.
+// It costs 4 d_b d_h FLOPs and 512 bytes (of workspace too) a cached row and head. The rows' number is
+// known on the device only; the host goes by the table's capacity, at most four times the query tokens,
+// which holds the workspace down: a sequence with many new tokens would gain behind any context at
+// d_b >= 256, and loses the form on wider tables.
+// Measured, whole calls, 128 heads, per-head against absorbed, ms. One prompt of 2048, 4096, 16384
+// tokens: d_b = 128: 0.24 and 0.31, 0.74 and 0.84, 9.45 and 9.13; d_b = 256: 0.27 and 0.66, 0.78 and
+// 1.90, 9.42 and 20.2; d_b = 512: 0.31 and 1.93, 0.86 and 6.61 (the first two). (A few calls at a time;
+// in long runs the power cap adds up to a tenth.) 1024 tokens on 4096 rows, a table at the rule's edge:
+// 0.35 and 0.31, 0.39 and 0.54, 0.47 and 2.69. So at d_b = 128 long prompts and chunks of longer
+// contexts lose 3 to 13 percent by it.
 bool per_head_sizes(const mlra_ctx* h, int total_q, int batch, int pt_stride) {
   if (h->summed || h->fp8 || h->var == kTiny) return false;
   const long long rows = (long long)batch * seq_rows_of(pt_stride);  // a row's index is 32 bits
