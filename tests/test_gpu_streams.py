@@ -134,3 +134,47 @@ def test_page_operators():
     assert lens.tolist() == [0, 0, 70] and refs.tolist()[:3] == [1, 0, 1]
     behind_queued_work(size, lambda s: M.mlra_compact_pages(hdl, inp["pool"], *state, stream=s))
     assert table[2].tolist() == [0, 1] and refs.tolist()[:3] == [1, 1, 0]
+
+
+def test_different_operators_at_once():
+    """Decode, prompt (both forms and few tokens), prefix and page calls on streams and workspaces of their
+    own, over one pool: the bits that each gives alone."""
+    w = W.scaled(W.WORKLOADS["mlra4_h128_b32_n8192"], batch=6, seq_len=None, len_range=(500, 900), seed=71)
+    inp = W.make_workload(w, device="cuda", extra_pages=40)
+    hdl = M.mlra_create(w.h, w.d_h, w.d_c, w.d_r, w.k, inp["w_uk"], inp["w_uv"])
+    pool, table, lens = inp["pool"], inp["page_table"], inp["seq_lens"]
+    q = torch.randn(1200, w.h, w.d_h + w.d_r, device="cuda").bfloat16()
+    size = lambda n: torch.empty(n, w.h, w.d_h, device="cuda")
+    P = 500
+    refs, rows, row_lens = i32([0] * P), i32([[-1] * 40] * 9), i32([0] * 9)
+    ids, new = i32([3, 1, 7]), i32([2000, 70, 2560])
+    part = (table[:, :3].contiguous(), torch.clamp(lens, max=192))
+    calls = [
+        (M.mlra_decode, (hdl, q[:6], pool, table, lens), size(6), M.mlra_workspace_size(hdl, 6)),
+        (M.mlra_prefill, (hdl, q, i32([0, 200, 400, 600, 800, 1000, 1200]), pool, *part), size(1200),
+         M.mlra_prefill_workspace_size(hdl, 1200, 6, 3)),
+        (M.mlra_prefill, (hdl, q[:100], i32([0, 10, 20, 30, 60, 99, 100]), pool, table, lens), size(100),
+         M.mlra_prefill_workspace_size(hdl, 100, 6, table.shape[1])),
+        (M.mlra_prefill, (hdl, q[:20], i32([0, 1, 2, 3, 10, 19, 20]), pool, table, lens), size(20),
+         M.mlra_prefill_workspace_size(hdl, 20, 6, table.shape[1])),
+        (M.mlra_decode_prefix, (hdl, q[:5], pool, table[:1].contiguous(), lens[:1].contiguous(), i32([0, 5]),
+                                table[1:].contiguous(), lens[1:].contiguous()), size(5),
+         M.mlra_decode_prefix_workspace_size(hdl, 5, 1)),
+    ]
+    workspaces = [torch.empty(n, dtype=torch.uint8, device="cuda") for *_, n in calls]
+    pages_ws = torch.empty(M.mlra_pages_workspace_size(hdl, P, 9), dtype=torch.uint8, device="cuda")
+    want = []
+    for (fn, args, out, _), ws in zip(calls, workspaces):
+        fn(*args, out, workspace=ws)
+        want.append(out.clone())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(len(calls) + 1)]
+    for _ in range(20):
+        for (fn, args, out, _), ws, s in zip(calls, workspaces, streams):
+            fn(*args, out, workspace=ws, stream=s)
+        M.mlra_reserve_pages(hdl, refs, rows, row_lens, ids, new, workspace=pages_ws, stream=streams[-1])
+        M.mlra_free_pages(hdl, refs, rows, row_lens, ids, workspace=pages_ws, stream=streams[-1])
+    torch.cuda.synchronize()
+    for (_, _, out, _), ws, ref in zip(calls, workspaces, want):
+        assert M.mlra_get_status(ws) == 0 and torch.equal(out, ref)
+    assert M.mlra_get_status(pages_ws) == 0 and not refs.any() and not row_lens.any()
