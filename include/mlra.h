@@ -295,7 +295,8 @@ int mlra_decode_prefix_workspace_size(mlra_handle h, int batch, int groups, size
  *                 MLRA_ERR_SEQ_LEN and every sequence is then decoded without a prefix.
  *   seq_lens      own rows only, may be 0; a sequence with neither gives o = 0, lse = -inf.
  * Other arguments as in mlra_decode; workspace >= mlra_decode_prefix_workspace_size bytes. bf16
- * caches only (MLRA_ERR_UNSUPPORTED with cache_fp8); batch <= 4096, groups <= 4096. */
+ * caches only (MLRA_ERR_UNSUPPORTED with cache_fp8); 1 <= batch <= 4096, 1 <= groups <= 4096 (a step
+ * without prefixes: one group of no rows, or mlra_decode). */
 int mlra_decode_prefix(mlra_handle h, const void* q, mlra_dtype q_dtype, const void* pool, int num_pages,
                        const int32_t* prefix_table, int prefix_stride, const int32_t* prefix_lens,
                        const int32_t* group_offsets, int groups, const int32_t* page_table, int pt_stride,

@@ -4,6 +4,10 @@ Argument marshalling only: every step of the decode runs in the library's CUDA k
 PyTorch supplies device memory and streams. The functions carry the C ABI's names
 (include/mlra.h) and raise ``MlraError`` on a non-zero status.
 
+A call runs on `stream` (None: the current one) and takes a workspace that it is not given from that
+stream's pool. The caller orders the stream behind the work that wrote the call's tensors, and records
+it on tensors that may be freed before it is done (torch.Tensor.record_stream).
+
 There is no CPU fallback: importing works without a GPU (so the library's exports can be
 checked), but any compute call needs the built library and a B200.
 """
